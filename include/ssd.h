@@ -70,6 +70,9 @@ enum { SSD_FANOUT_GEOMETRIC = 0, SSD_FANOUT_UNIFORM = 1 };
 /* Limits of this build. */
 #define SSD_MAX_K 32              /* draft length K */
 #define SSD_MAX_BUDGET 512        /* fan-out branch budget (total cache keys per row) */
+#define SSD_MAX_TOP 256           /* teacher logits kept per row (ssd_teacher_top, ssd_distill) */
+#define SSD_MIN_TRAIN_T 1e-4f     /* temperatures of ssd_teacher_top and ssd_distill */
+#define SSD_MAX_TRAIN_T 1e4f
 
 /*
  * Speculation cache of one batch ([ZH] section 2, basic flow step 3; [NL]
@@ -332,6 +335,71 @@ ssd_status ssd_cache_lookup(const int32_t* offsets, const int32_t* tokens, int B
                             int budget, const int32_t* k, const int32_t* bonus,
                             const int32_t* payload, uint64_t fallback_seed, int V,
                             uint8_t* hit, int32_t* slot, int32_t* next_tokens, void* stream);
+
+/*
+ * Draft training.  The acceptance alpha, and with it the yield of every call
+ * above, is set by how close the draft q is to the target p ([ZH] section 1:
+ * lossless verification accepts by p / q; section 2, challenge 1: the split
+ * follows the acceptance).  The pages describe no training step; these calls
+ * exist for callers that train the draft on what the target answered: the
+ * target's logits that a verify step had in hand, kept as each row's top M
+ * (ssd_teacher_top), a distillation loss of the draft's rows against them with
+ * its gradient (ssd_distill), and the cross entropy of the draft's linear head
+ * on accepted tokens with its gradients (ssd_linear_ce, ssd_linear_ce_grad).
+ *
+ * Row tensors of ssd_teacher_top and ssd_distill are [n_batch,
+ * rows_per_batch, V] views: row (b, j) starts at element b * batch_stride +
+ * j * row_stride, tokens are adjacent, and rows may start at any element (no
+ * 16-byte rule).  So the K draft positions of target logits [B, K+1, V] are
+ * (B, K, V) with batch_stride (K+1) V; other per-row arrays are dense, row
+ * b * rows_per_batch + j.  One cluster of thread blocks stages a whole row in
+ * shared memory: rows of up to 1.6 MB (V <= 400000 fp32, 800000 bf16), else
+ * SSD_ERR_UNSUPPORTED.  SSD_MIN_TRAIN_T <= T <= SSD_MAX_TRAIN_T.  Results are
+ * the same bits on every call.
+ */
+
+/*
+ * ssd_teacher_top -- each row's M largest logits and the mass around them:
+ *   tokens [rows, M] out: ids by raw logit descending, ties to the lower id
+ *   (-0 = +0); values [rows, M] out: their raw logits; lse [rows] out: log
+ *   sum_v exp(l(v)/T); tail [rows] out: the same sum over the tokens that are
+ *   not among the M (-inf when there are none), formed without subtraction.
+ *   1 <= M <= min(V, SSD_MAX_TOP).  status [rows] out: SSD_ROW_NONFINITE for a
+ *   row with a NaN or +inf logit or all of -inf (tokens -1, the rest NaN).
+ */
+ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_per_batch, int V,
+                           int64_t batch_stride, int64_t row_stride, float T, int M, int32_t* tokens,
+                           float* values, float* lse, float* tail, int32_t* status, void* stream);
+
+/*
+ * ssd_distill -- distillation loss of student rows z against a teacher of M
+ * atoms and a tail, and its gradient.  The teacher's weights are p = softmax
+ * over (values[m] / T, tail); q = softmax(z / T), q_tail = sum of q over the
+ * tokens that are no atom:
+ *   loss = sum_m p_m log(p_m / q_m) + p_tail log(p_tail / q_tail)
+ *   grad[v] = row_scale / T * (q_v - p_m)                 at v = tokens[m]
+ *             row_scale / T * (q_tail - p_tail) q_v / q_tail    elsewhere
+ * With ssd_teacher_top's tokens, values and tail at the same T this is the
+ * divergence between target and draft with the target's tail as one event;
+ * with tail NULL (or -inf) the top is renormalised and q stays whole.
+ *   tokens [rows, M]: distinct ids, -1 for an absent atom; values [rows, M]
+ *   (-inf: no weight); tail [rows] or NULL.  row_scale [rows] or NULL (1): the
+ *   factor of the row's gradient (loss is not scaled).  A row of row_scale 0
+ *   is left out: its logits and teacher are not read, loss 0, gradient 0.
+ *   loss [rows], status [rows] out.  grad: NULL, or the gradient with respect
+ *   to the logits, in their dtype, [n_batch, rows_per_batch, V] with its own
+ *   strides; it may be the logits themselves (same pointer and strides), and
+ *   its rows must not overlap.
+ *   status: SSD_ROW_NONFINITE (NaN or +inf among a row's logits, values or
+ *   tail, all logits -inf, or a teacher without weight), SSD_ROW_BAD_TOKEN (an
+ *   id outside [-1, V) or twice in a row): loss NaN, gradient 0.
+ *   SSD_ROW_ZERO_Q (informational): q is 0 where p is not; the loss is +inf.
+ */
+ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_batch, int V,
+                       int64_t batch_stride, int64_t row_stride, float T, int M, const int32_t* tokens,
+                       const float* values, const float* tail, const float* row_scale, float* loss,
+                       int32_t* status, void* grad, int64_t grad_batch_stride, int64_t grad_row_stride,
+                       void* stream);
 
 /* Workspace size in bytes for ssd_verify / ssd_saguaro_reweight at
  * (B, K, V, dtype).  The workspace holds per-slice and per-(row, position)

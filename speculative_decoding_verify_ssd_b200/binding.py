@@ -34,6 +34,7 @@ ROW_INVALID = ROW_NONFINITE | ROW_BAD_TOKEN | ROW_BAD_UNIFORM | ROW_BAD_PLAN | R
 
 MAX_K = 32
 MAX_BUDGET = 512
+MAX_TOP = 256
 
 
 class SsdError(RuntimeError):
@@ -99,6 +100,10 @@ def load(build_if_missing: bool = True):
     L.ssd_cache_build.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp]
     L.ssd_cache_lookup.restype = i32
     L.ssd_cache_lookup.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, C.c_uint64, i32, vp, vp, vp, vp]
+    L.ssd_teacher_top.restype = i32
+    L.ssd_teacher_top.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp]
+    L.ssd_distill.restype = i32
+    L.ssd_distill.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp]
     _lib = L
     return L
 
@@ -518,3 +523,94 @@ def ssd_cache_lookup(offsets: torch.Tensor, tokens: torch.Tensor, k: torch.Tenso
                                        _ptr(payload), fallback_seed, V, _ptr(hit), _ptr(slot), _ptr(nxt),
                                        _stream(stream)), "ssd_cache_lookup")
     return hit, slot, nxt
+
+
+# ---------------------------------------------------------------------------
+# Draft training.
+# ---------------------------------------------------------------------------
+def _rows_of(t: torch.Tensor, name: str):
+    """(n_batch, rows_per_batch, V, batch_stride, row_stride) of a [V], [R, V]
+    or [B, R, V] view whose last dimension is dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() not in (1, 2, 3):
+        raise ValueError(f"{name} must have one to three dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    lead, strides = (1, 1) + tuple(t.shape[:-1]), (0, 0) + tuple(t.stride()[:-1])
+    return lead[-2], lead[-1], t.shape[-1], strides[-2], strides[-1]
+
+
+def _stream_scope(device, stream):
+    """The device, and `stream` (or the device's current one) as the stream that
+    the call's own allocations belong to."""
+    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+
+
+@dataclass
+class TeacherTop:
+    tokens: torch.Tensor
+    values: torch.Tensor
+    lse: torch.Tensor
+    tail: torch.Tensor
+    status: torch.Tensor
+
+
+def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -> TeacherTop:
+    """Top-M logits of every row of `logits` ([..., V], up to three dimensions,
+    e.g. target[:, :K]) with the log-mass of all and of the other tokens (see
+    ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
+    nb, rpb, V, bs, rs = _rows_of(logits, "logits")
+    dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
+    with torch.cuda.device(dev), _stream_scope(dev, stream):
+        M = int(M)
+        f32 = dict(dtype=torch.float32, device=dev)
+        r = TeacherTop(tokens=torch.empty(lead + (max(M, 0),), dtype=torch.int32, device=dev),
+                       values=torch.empty(lead + (max(M, 0),), **f32), lse=torch.empty(lead, **f32),
+                       tail=torch.empty(lead, **f32), status=torch.empty(lead, dtype=torch.int32, device=dev))
+        _check(load().ssd_teacher_top(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(r.tokens),
+                                      _ptr(r.values), _ptr(r.lse), _ptr(r.tail), _ptr(r.status), _stream()),
+               "ssd_teacher_top")
+    return r
+
+
+@dataclass
+class DistillResult:
+    loss: torch.Tensor
+    status: torch.Tensor
+    grad: Optional[torch.Tensor] = None
+
+
+def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor,
+                tail: Optional[torch.Tensor] = None, T: float = 1.0, row_scale: Optional[torch.Tensor] = None,
+                with_grad: bool = True, grad: Optional[torch.Tensor] = None, stream=None) -> DistillResult:
+    """Distillation loss of the rows of `logits` ([..., V], up to three
+    dimensions) against a teacher's atoms and tail, and its gradient (see
+    ssd_distill in ssd.h).  `grad` may be given (of the logits' shape and dtype,
+    dense in its last dimension; the logits themselves are allowed)."""
+    nb, rpb, V, bs, rs = _rows_of(logits, "logits")
+    dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
+    M = tokens.shape[-1] if tokens.dim() else 0
+    _need(tokens, "tokens", torch.int32, lead + (M,), dev)
+    _need(values, "values", torch.float32, lead + (M,), dev)
+    if tail is not None:
+        _need(tail, "tail", torch.float32, lead, dev)
+    if row_scale is not None:
+        _need(row_scale, "row_scale", torch.float32, lead, dev)
+    if grad is not None:
+        if not with_grad:
+            raise ValueError("grad is given but with_grad is False")
+        if grad.dtype != logits.dtype or grad.device != dev or grad.shape != logits.shape:
+            raise ValueError("grad must have the logits' shape, dtype and device")
+    with torch.cuda.device(dev), _stream_scope(dev, stream):
+        if with_grad and grad is None:
+            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        gbs, grs = _rows_of(grad, "grad")[3:] if with_grad else (0, 0)
+        r = DistillResult(loss=torch.empty(lead, dtype=torch.float32, device=dev),
+                          status=torch.empty(lead, dtype=torch.int32, device=dev), grad=grad)
+        _check(load().ssd_distill(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(tokens), _ptr(values),
+                                  _ptr(tail), _ptr(row_scale), _ptr(r.loss), _ptr(r.status), _ptr(grad), gbs, grs,
+                                  _stream()), "ssd_distill")
+    return r
