@@ -73,6 +73,9 @@ enum { SSD_FANOUT_GEOMETRIC = 0, SSD_FANOUT_UNIFORM = 1 };
 #define SSD_MAX_TOP 256           /* teacher logits kept per row (ssd_teacher_top, ssd_distill) */
 #define SSD_MIN_TRAIN_T 1e-4f     /* temperatures of ssd_teacher_top and ssd_distill */
 #define SSD_MAX_TRAIN_T 1e4f
+#define SSD_MAX_LINEAR_N (1 << 20) /* rows, width and vocabulary of ssd_linear_ce */
+#define SSD_MAX_LINEAR_D (1 << 16)
+#define SSD_MAX_LINEAR_V (1 << 24)
 
 /*
  * Speculation cache of one batch ([ZH] section 2, basic flow step 3; [NL]
@@ -400,6 +403,54 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
                        const float* values, const float* tail, const float* row_scale, float* loss,
                        int32_t* status, void* grad, int64_t grad_batch_stride, int64_t grad_row_stride,
                        void* stream);
+
+/*
+ * ssd_linear_ce -- cross entropy of the draft's linear head on hard targets,
+ * logits z = hidden weight^T formed tile by tile and never stored:
+ *   loss[n] = lse[n] - z[n, targets[n]],  lse[n] = log sum_v exp(z[n, v]).
+ *   hidden [n_batch, rows_per_batch, D] bf16 (row (b, j) at element b *
+ *   batch_stride + j * row_stride), weight [V, D] bf16 (rows weight_stride
+ *   apart), dtype SSD_DTYPE_BF16.  D and the strides are multiples of 8, the
+ *   base pointers 16-byte aligned.  N = n_batch * rows_per_batch.  Products are
+ *   summed in fp32.  targets [N]: a negative one leaves the row out (loss and
+ *   lse 0; its hidden state is not read), so ssd_verify's out_tokens, -1 behind
+ *   the bonus, are targets as they are.  loss, lse, status [N] out:
+ *   SSD_ROW_BAD_TOKEN (target >= V), SSD_ROW_NONFINITE (NaN or infinite
+ *   logits): loss and lse NaN.
+ *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 0) bytes, 256-byte
+ *   aligned; it needs no initial contents, and calls that overlap on the GPU
+ *   must not share one.  Results are the same bits on every call.
+ */
+ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int n_batch, int rows_per_batch,
+                         int D, int V, int64_t batch_stride, int64_t row_stride, int64_t weight_stride,
+                         const int32_t* targets, float* loss, float* lse, int32_t* status, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * ssd_linear_ce_grad -- the gradients of sum_n row_scale[n] loss[n]:
+ *   G[n, v] = row_scale[n] (exp(z[n, v] - lse[n]) - [v = targets[n]]),
+ *   grad_hidden = G weight, grad_weight = G^T hidden.
+ *   z is formed again, one piece of the vocabulary at a time; G is rounded to
+ *   bf16 (relative 2^-8, the rounding of the results) for the two products,
+ *   which are summed in fp32 and rounded once.  hidden, weight, targets and
+ *   strides as in ssd_linear_ce, lse [N] as it wrote it; row_scale [N] or NULL
+ *   (1).  grad_hidden [N, D] out, grad_weight [V, D] out, bf16, dense,
+ *   16-byte aligned; every element is written.  Rows with a negative target or
+ *   row_scale 0 have no part and grad_hidden 0, nor have rows with a target
+ *   >= V or an lse that is not finite.  status [N] out, or NULL: those last
+ *   two, as ssd_linear_ce names them.
+ *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 1) bytes, otherwise as in
+ *   ssd_linear_ce.
+ */
+ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype, int n_batch,
+                              int rows_per_batch, int D, int V, int64_t batch_stride, int64_t row_stride,
+                              int64_t weight_stride, const int32_t* targets, const float* lse,
+                              const float* row_scale, void* grad_hidden, void* grad_weight, int32_t* status,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace size of ssd_linear_ce (grad 0) and ssd_linear_ce_grad (grad 1) at
+ * N rows; 0 for invalid sizes. */
+size_t ssd_linear_ce_workspace_bytes(int N, int D, int V, int grad);
 
 /* Workspace size in bytes for ssd_verify / ssd_saguaro_reweight at
  * (B, K, V, dtype).  The workspace holds per-slice and per-(row, position)

@@ -7,6 +7,7 @@ in libssd's CUDA kernels; there is no CPU path.  Functions keep the C names.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -104,6 +105,13 @@ def load(build_if_missing: bool = True):
     L.ssd_teacher_top.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp]
     L.ssd_distill.restype = i32
     L.ssd_distill.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp]
+    L.ssd_linear_ce_workspace_bytes.restype = sz
+    L.ssd_linear_ce_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.ssd_linear_ce.restype = i32
+    L.ssd_linear_ce.argtypes = [vp, vp, i32, i32, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.ssd_linear_ce_grad.restype = i32
+    L.ssd_linear_ce_grad.argtypes = [vp, vp, i32, i32, i32, i32, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz,
+                                     vp]
     _lib = L
     return L
 
@@ -543,10 +551,10 @@ def _rows_of(t: torch.Tensor, name: str):
     return lead[-2], lead[-1], t.shape[-1], strides[-2], strides[-1]
 
 
-def _stream_scope(device, stream):
-    """The device, and `stream` (or the device's current one) as the stream that
-    the call's own allocations belong to."""
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+def _stream_scope(stream):
+    """`stream`, when one is given, as the stream that the call's own
+    allocations belong to."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 @dataclass
@@ -564,7 +572,7 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
     dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
-    with torch.cuda.device(dev), _stream_scope(dev, stream):
+    with torch.cuda.device(dev), _stream_scope(stream):
         M = int(M)
         f32 = dict(dtype=torch.float32, device=dev)
         r = TeacherTop(tokens=torch.empty(lead + (max(M, 0),), dtype=torch.int32, device=dev),
@@ -604,7 +612,7 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
             raise ValueError("grad is given but with_grad is False")
         if grad.dtype != logits.dtype or grad.device != dev or grad.shape != logits.shape:
             raise ValueError("grad must have the logits' shape, dtype and device")
-    with torch.cuda.device(dev), _stream_scope(dev, stream):
+    with torch.cuda.device(dev), _stream_scope(stream):
         if with_grad and grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         gbs, grs = _rows_of(grad, "grad")[3:] if with_grad else (0, 0)
@@ -614,3 +622,81 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
                                   _ptr(tail), _ptr(row_scale), _ptr(r.loss), _ptr(r.status), _ptr(grad), gbs, grs,
                                   _stream()), "ssd_distill")
     return r
+
+
+def linear_ce_workspace_bytes(N: int, D: int, V: int, grad: bool) -> int:
+    return int(load().ssd_linear_ce_workspace_bytes(N, D, V, int(grad)))
+
+
+def _linear_args(hidden, weight, targets):
+    nb, rpb, D, bs, rs = _rows_of(hidden, "hidden")
+    dev = hidden.device
+    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise ValueError("hidden and weight must be torch.bfloat16")
+    if weight.device != dev:
+        raise ValueError(f"weight must be on {dev}, got {weight.device}")
+    if weight.dim() != 2 or weight.shape[1] != D or weight.stride(1) != 1:
+        raise ValueError(f"weight must be [V, {D}] and dense in its last dimension")
+    _need(targets, "targets", torch.int32, tuple(hidden.shape[:-1]), dev)
+    V = weight.shape[0]
+    return dev, nb * rpb, V, (_ptr(hidden), _ptr(weight), DTYPE_BF16, nb, rpb, D, V, bs, rs,
+                              weight.stride(0) if V > 1 else max(weight.stride(0), D), _ptr(targets))
+
+
+def _linear_workspace(workspace, N, D, V, grad, dev):
+    """The caller's workspace (a uint8 tensor), or one of the caching allocator:
+    it belongs to the current stream, or to the graph that is being captured."""
+    if workspace is None:
+        return torch.empty(max(linear_ce_workspace_bytes(N, D, V, grad), 1), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense torch.uint8 tensor on {dev}")
+    return workspace
+
+
+@dataclass
+class LinearCeResult:
+    loss: torch.Tensor
+    lse: torch.Tensor
+    status: torch.Tensor
+
+
+def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> LinearCeResult:
+    """Cross entropy of the rows of hidden @ weight.T against `targets`
+    (negative: left out), without storing the logits (see ssd_linear_ce in
+    ssd.h).  hidden [..., D] (up to three dimensions) and weight [V, D] bf16."""
+    dev, N, V, args = _linear_args(hidden, weight, targets)
+    with torch.cuda.device(dev), _stream_scope(stream):
+        ws = _linear_workspace(workspace, N, hidden.shape[-1], V, False, dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        r = LinearCeResult(loss=torch.empty(targets.shape, **f32), lse=torch.empty(targets.shape, **f32),
+                           status=torch.empty(targets.shape, dtype=torch.int32, device=dev))
+        _check(load().ssd_linear_ce(*args, _ptr(r.loss), _ptr(r.lse), _ptr(r.status), _ptr(ws), ws.numel(),
+                                    _stream()), "ssd_linear_ce")
+    return r
+
+
+def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                       row_scale: Optional[torch.Tensor] = None, grad_hidden: Optional[torch.Tensor] = None,
+                       grad_weight: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """(grad_hidden, grad_weight) of sum(row_scale * loss), loss and lse being
+    ssd_linear_ce's (see ssd_linear_ce_grad in ssd.h)."""
+    dev, N, V, args = _linear_args(hidden, weight, targets)
+    D = hidden.shape[-1]
+    _need(lse, "lse", torch.float32, tuple(targets.shape), dev)
+    if row_scale is not None:
+        _need(row_scale, "row_scale", torch.float32, tuple(targets.shape), dev)
+    if status is not None:
+        _need(status, "status", torch.int32, tuple(targets.shape), dev)
+    with torch.cuda.device(dev), _stream_scope(stream):
+        ws = _linear_workspace(workspace, N, D, V, True, dev)
+        if grad_hidden is None:
+            grad_hidden = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
+        if grad_weight is None:
+            grad_weight = torch.empty((V, D), dtype=torch.bfloat16, device=dev)
+        _need(grad_hidden, "grad_hidden", torch.bfloat16, tuple(hidden.shape), dev)
+        _need(grad_weight, "grad_weight", torch.bfloat16, (V, D), dev)
+        _check(load().ssd_linear_ce_grad(*args, _ptr(lse), _ptr(row_scale), _ptr(grad_hidden), _ptr(grad_weight),
+                                         _ptr(status), _ptr(ws), ws.numel(), _stream()), "ssd_linear_ce_grad")
+    return grad_hidden, grad_weight

@@ -1,0 +1,693 @@
+// ssd_linear.cuh -- the cross entropy of a linear head and its gradients
+// without stored logits (ssd_linear_ce, ssd_linear_ce_grad): one persistent
+// tcgen05 matrix-product kernel in four forms that differ in which operands
+// they read and in what their epilogue does with a tile.
+//
+//   lse   z = H W^T            -> per row and vocabulary tile: max, sum exp(z - max); the target's logit
+//   grad  G = s (softmax(z) - onehot)  in bf16, one piece of the vocabulary at a time
+//   dh    dH += G W            -> fp32, one slot per split of the piece
+//   dw    dW = G^T H           -> bf16
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ssd.h"
+#include "ssd_device.cuh"
+#include "ssd_rows.cuh"
+
+namespace ssd {
+
+constexpr int kGemmThreads = 192;  // warp 0: copies, warp 1: products, warps 2-5: epilogue
+constexpr int kTileN = 256;        // accumulator columns
+constexpr int kBlockK = 64;        // one 128-byte swizzle row of bf16
+constexpr int kATile = 128 * kBlockK * 2;
+constexpr int kOutBuf = 32 * 128;  // one epilogue warp's staging buffer: 32 rows of 128 bytes
+constexpr unsigned long long kGemmWaitNs = 2000000000ull;
+
+enum GemmOp { kOpLse = 0, kOpGrad = 1, kOpDh = 2, kOpDw = 3 };
+
+template <int CG>
+struct GemmShape {
+  static constexpr int kTileM = 128 * CG;
+  static constexpr int kBRows = kTileN / CG;  // the CTA's share of the B tile
+  static constexpr int kBTile = kBRows * kBlockK * 2;
+  static constexpr int kStage = kATile + kBTile;
+  static constexpr int kStages = CG == 1 ? 4 : 6;
+  static constexpr int kSmem = kStages * kStage + 4 * 2 * kOutBuf + 1024;  // and the slack to align to 1 KB
+};
+
+// The head of the workspace.
+struct LinearHdr {
+  int32_t n_active, error;
+};
+
+struct GemmArgs {
+  const LinearHdr* hdr;
+  int32_t* error;
+  const int32_t* target;  // per active row
+  const float* scale;
+  const float* lse;
+  float* zt;        // the target's logit per active row
+  float2* part;     // [vocabulary tile][rows]
+  int rows;         // padded row count: leading dimension of part, rows of one dh slot
+  int V, D;
+  int v0, v_count;  // the piece of the vocabulary
+  int slots, first; // dh: splits of the piece; whether it is the first piece
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05, tensor copies.
+// ---------------------------------------------------------------------------
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* out, uint32_t cols) {
+  if (CG == 1)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)), "r"(cols)
+                 : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)), "r"(cols)
+                 : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if (CG == 1) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  } else {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+  }
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major (rows of 64 k):
+// groups of 8 rows lie 1024 bytes apart.  MN-major (rows of 64 m or n, one per
+// k): groups of 8 k lie 1024 bytes apart, the next 64 m or n 8192 bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major) {
+  const uint64_t lbo = mn_major ? (8192u >> 4) : 1u;
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (lbo << 16) | (static_cast<uint64_t>(1024u >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on the barrier (in both CTAs of a pair) when the products issued so
+// far have completed.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if (CG == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// The address of a shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+
+// Tile load into this CTA's shared memory; the bytes are counted on the
+// barrier at cluster address `bar` (the pair's first CTA when CG = 2).
+template <int CG>
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(y), "r"(smem_addr(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(smem_addr(src))
+               : "memory");
+}
+
+// 32 consecutive accumulator columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// A wait of one of the kernel's roles.  Once one has given up, the kernel's
+// other waits in this CTA give up too, and the call is flagged.
+struct GemmWait {
+  volatile int* abort;
+  int32_t* error;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 0; i < (1u << 30); ++i) {
+      if (mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
+      if (*abort || global_ns() - t0 > kGemmWaitNs) break;
+    }
+    *abort = 1;
+    atomicExch(error, 1);
+    return false;
+  }
+};
+
+// One tile of a form's work list.
+struct GemmTile {
+  int m, n, slot, kb0, kb1;
+};
+
+template <int Op, int CG>
+struct GemmWork {
+  int m_tiles, n_tiles, k_blocks, count;
+  __device__ __forceinline__ GemmWork(const GemmArgs& a, int n_active) {
+    const int na = max(n_active, 1);
+    constexpr int TM = GemmShape<CG>::kTileM;
+    if (Op == kOpDw) {
+      m_tiles = (a.v_count + TM - 1) / TM;
+      n_tiles = (a.D + kTileN - 1) / kTileN;
+      k_blocks = (na + kBlockK - 1) / kBlockK;
+    } else {
+      m_tiles = (na + TM - 1) / TM;
+      n_tiles = ((Op == kOpDh ? a.D : a.v_count) + kTileN - 1) / kTileN;
+      k_blocks = ((Op == kOpDh ? a.v_count : a.D) + kBlockK - 1) / kBlockK;
+    }
+    count = m_tiles * n_tiles * (Op == kOpDh ? a.slots : 1);
+  }
+  // Neighbouring tiles share the operand that is dear: the weight tile (lse,
+  // grad, dh), or the piece's columns (dw).
+  __device__ __forceinline__ GemmTile at(const GemmArgs& a, int t) const {
+    GemmTile r;
+    r.slot = 0;
+    if (Op == kOpDw) {
+      r.n = t % n_tiles;
+      r.m = t / n_tiles;
+    } else {
+      if (Op == kOpDh) {
+        r.slot = t / (m_tiles * n_tiles);
+        t -= r.slot * m_tiles * n_tiles;
+      }
+      r.m = t % m_tiles;
+      r.n = t / m_tiles;
+    }
+    r.kb0 = 0;
+    r.kb1 = k_blocks;
+    if (Op == kOpDh) {
+      r.kb0 = static_cast<int>(static_cast<long long>(k_blocks) * r.slot / a.slots);
+      r.kb1 = static_cast<int>(static_cast<long long>(k_blocks) * (r.slot + 1) / a.slots);
+    }
+    return r;
+  }
+};
+
+// r[i], by halving: registers have no index.
+__device__ __forceinline__ uint32_t pick32(const uint32_t (&r)[32], int i) {
+  uint32_t v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = (i & 16) ? r[j + 16] : r[j];
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) v[j] = (i & w) ? v[j + w] : v[j];
+  return v[0];
+}
+
+// Stages 16 bytes of the lane's row (128 bytes, 128-byte swizzle).
+__device__ __forceinline__ void stage16(char* buf, int lane, int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  *reinterpret_cast<uint4*>(buf + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(x, y, z, w);
+}
+
+template <int Op, int CG>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    ssd_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_out, const GemmArgs a) {
+  using S = GemmShape<CG>;
+  constexpr int kStages = S::kStages;
+  constexpr bool kAMn = Op == kOpDw, kBMn = Op == kOpDh || Op == kOpDw;
+  extern __shared__ char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  char* out_buf = smem + kStages * S::kStage;
+  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 4 * CG);
+    }
+    abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<CG>(&tmem_base, 512);
+  tc_fence_before();
+  if (CG == 1)
+    __syncthreads();
+  else
+    cg::this_cluster().sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const GemmWait wait = {&abort_flag, a.error};
+  const int n_active = a.hdr->n_active;
+  const GemmWork<Op, CG> work(a, n_active);
+  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < work.count; t += step) {
+        const GemmTile tile = work.at(a, t);
+        const int m0 = tile.m * S::kTileM + rank * 128, n0 = tile.n * kTileN + rank * S::kBRows;
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+          if (!wait(&empty[s], phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          char* pa = smem + s * S::kStage;
+          char* pb = pa + kATile;
+          const int k0 = kb * kBlockK;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * CG);
+          const uint32_t bar = CG == 1 ? smem_addr(&full[s]) : cluster_addr(&full[s], 0);
+          if (kAMn) {
+            tma_load<CG>(pa, &map_a, m0, k0, bar);
+            tma_load<CG>(pa + 8192, &map_a, m0 + 64, k0, bar);
+          } else {
+            tma_load<CG>(pa, &map_a, k0, m0, bar);
+          }
+          if (kBMn) {
+            const int y = k0 + (Op == kOpDh ? a.v0 : 0);
+#pragma unroll
+            for (int j = 0; j < S::kBRows / 64; ++j) tma_load<CG>(pb + j * 8192, &map_b, n0 + j * 64, y, bar);
+          } else {
+            tma_load<CG>(pb, &map_b, k0, a.v0 + n0, bar);
+          }
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // D fp32, A and B bf16, majorness, N / 8, M / 16
+      constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
+                                 (static_cast<uint32_t>(kTileN / 8) << 17) |
+                                 (static_cast<uint32_t>(S::kTileM / 16) << 24);
+      int s = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < work.count; t += step) {
+        const GemmTile tile = work.at(a, t);
+        if (tile.kb0 == tile.kb1) continue;
+        if (!wait(&tempty[acc], acc_phase ^ 1)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * kTileN;
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+          if (!wait(&full[s], phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t pa = smem_addr(smem + s * S::kStage);
+          const uint64_t da = operand_desc(pa, kAMn), db = operand_desc(pa + kATile, kBMn);
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k)
+            mma_bf16<CG>(d, da + static_cast<uint64_t>(k * ((kAMn ? 2048 : 32) >> 4)),
+                         db + static_cast<uint64_t>(k * ((kBMn ? 2048 : 32) >> 4)), idesc,
+                         (kb > tile.kb0 || k > 0) ? 1u : 0u);
+          mma_commit<CG>(&empty[s]);
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) mma_commit<CG>(&tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+    }
+  } else {
+    // Epilogue: warp w reads the accumulator lanes 32 (w mod 4) .. + 31.
+    const int quad = warp & 3;
+    char* buf = out_buf + (warp - 2) * 2 * kOutBuf;
+    int acc = 0, b = 0;
+    uint32_t acc_phase = 0;
+    for (int t = first; t < work.count; t += step) {
+      const GemmTile tile = work.at(a, t);
+      if (tile.kb0 == tile.kb1) continue;
+      const int row = tile.m * S::kTileM + rank * 128 + quad * 32 + lane;  // of the product
+      const int row0 = row - lane;
+      bool live = true;
+      int target = -1;
+      float scale = 0.f, shift = 0.f;
+      if (Op == kOpLse || Op == kOpGrad) {
+        live = row < n_active;
+        if (live) target = a.target[row] - a.v0 - tile.n * kTileN;
+        if (Op == kOpGrad && live) {
+          scale = a.scale[row];
+          shift = a.lse[row] * kLog2e;
+        }
+      }
+      const int n_valid = a.v_count - tile.n * kTileN;  // lse, grad: columns inside the vocabulary
+      if (!wait(&tfull[acc], acc_phase)) break;
+      tc_fence_after();
+      const uint32_t src = tmem + acc * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < kTileN / 32; ++c) {
+        uint32_t r[32];
+        tmem_load32(src + c * 32, r);
+        if (Op == kOpLse) {
+          if (c * 32 + 32 > n_valid) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j >= n_valid) r[j] = 0xFF800000u;
+          }
+          float m = mx;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(r[j]));
+          const float ref = m > -INFINITY ? m : 0.f;
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) add[j & 3] += ex2((__uint_as_float(r[j]) - ref) * kLog2e);
+          sum = sum * ex2((mx - ref) * kLog2e) + ((add[0] + add[1]) + (add[2] + add[3]));
+          mx = m;
+          if (target >= 0 && (target >> 5) == c) a.zt[row] = __uint_as_float(pick32(r, target & 31));
+        } else if (Op == kOpGrad) {
+          float g[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float p = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -shift));
+            if (target == c * 32 + j) p -= 1.f;
+            g[j] = live && c * 32 + j < n_valid ? p * scale : 0.f;
+          }
+          const int half = c & 1;
+          if (half == 0) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            stage16(buf + b * kOutBuf, lane, half * 4 + q, Elem<uint16_t>::pack2(g[q * 8], g[q * 8 + 1]),
+                    Elem<uint16_t>::pack2(g[q * 8 + 2], g[q * 8 + 3]), Elem<uint16_t>::pack2(g[q * 8 + 4], g[q * 8 + 5]),
+                    Elem<uint16_t>::pack2(g[q * 8 + 6], g[q * 8 + 7]));
+          if (half == 1) {
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store(&map_out, tile.n * kTileN + (c >> 1) * 64, row0, buf + b * kOutBuf);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            b ^= 1;
+          }
+        } else if (Op == kOpDh) {
+          if (tile.n * kTileN + c * 32 < a.D) {  // uniform over the warp
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              stage16(buf + b * kOutBuf, lane, q, r[q * 4], r[q * 4 + 1], r[q * 4 + 2], r[q * 4 + 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              const int x = tile.n * kTileN + c * 32, y = tile.slot * a.rows + row0;
+              if (a.first)
+                tma_store(&map_out, x, y, buf + b * kOutBuf);
+              else
+                tma_add(&map_out, x, y, buf + b * kOutBuf);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            b ^= 1;
+          }
+        } else {
+          const int half = c & 1;
+          if (tile.n * kTileN + (c >> 1) * 64 < a.D && a.v0 + row0 < a.V) {  // uniform over the warp
+            if (half == 0) {
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+              __syncwarp();
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              stage16(buf + b * kOutBuf, lane, half * 4 + q,
+                      Elem<uint16_t>::pack2(__uint_as_float(r[q * 8]), __uint_as_float(r[q * 8 + 1])),
+                      Elem<uint16_t>::pack2(__uint_as_float(r[q * 8 + 2]), __uint_as_float(r[q * 8 + 3])),
+                      Elem<uint16_t>::pack2(__uint_as_float(r[q * 8 + 4]), __uint_as_float(r[q * 8 + 5])),
+                      Elem<uint16_t>::pack2(__uint_as_float(r[q * 8 + 6]), __uint_as_float(r[q * 8 + 7])));
+            if (half == 1) {
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store(&map_out, tile.n * kTileN + (c >> 1) * 64, a.v0 + row0, buf + b * kOutBuf);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+              }
+              b ^= 1;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1)
+          asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&tempty[acc])) : "memory");
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           cluster_addr(&tempty[acc], 0))
+                       : "memory");
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+      if (Op == kOpLse && live) a.part[static_cast<size_t>(tile.n) * a.rows + row] = make_float2(mx, sum);
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();
+  if (abort_flag) {  // copies and products may still be in flight: far longer than any of them takes
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < 100000 && global_ns() - t0 < 20000000ull; ++i) __nanosleep(1000);
+    __syncthreads();
+  }
+  if (CG == 2) cg::this_cluster().sync();  // the pair's barriers and accumulators are no longer used
+  if (warp == 1) tmem_free<CG>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Before and after the products.
+// ---------------------------------------------------------------------------
+struct PrepArgs {
+  LinearHdr* hdr;
+  RowsIn hidden;
+  const int32_t* targets;
+  const float* row_scale;  // gradient call only; may be NULL
+  const float* lse;        // gradient call only
+  int32_t* index;          // the active rows' places among the N
+  int32_t* target;         // their targets, scales, log-normalisers
+  float* scale;
+  float* lse_c;
+  uint16_t* h;             // their hidden states, dense, zero rows behind the last up to a tile's end
+  float* loss;             // forward call: what left-out rows get
+  float* lse_out;
+  uint16_t* grad_hidden;   // gradient call: likewise
+  int32_t* status;         // may be NULL in the gradient call
+  int N, V, D, tile_m;
+};
+
+constexpr int kPrepRows = 32;  // rows of one block
+
+// Whether row n takes part, and its status where it does not.  A row whose
+// log-normaliser is not finite is left out of the gradient: its NaN would reach
+// every row of the weight's gradient.
+__device__ __forceinline__ bool row_active(const PrepArgs& a, int n, int32_t* status) {
+  const int t = a.targets[n];
+  *status = 0;
+  if (t < 0) return false;
+  if (a.row_scale && a.row_scale[n] == 0.f) return false;
+  if (t >= a.V) {
+    *status = SSD_ROW_BAD_TOKEN;
+    return false;
+  }
+  if (a.lse && !(fabsf(a.lse[n]) < INFINITY)) {
+    *status = SSD_ROW_NONFINITE;
+    return false;
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const PrepArgs a) {
+  __shared__ int ired[kRowWarps];
+  __shared__ int place[kPrepRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = static_cast<int>(blockIdx.x) * kPrepRows;
+  int before = 0, total = 0;
+  int32_t st;
+  for (int n = tid; n < a.N; n += kRowThreads) {
+    const int on = row_active(a, n, &st) ? 1 : 0;
+    total += on;
+    if (n < n0) before += on;
+  }
+  before = block_reduce(before, ired, OpAdd());
+  total = block_reduce(total, ired, OpAdd());
+  if (blockIdx.x == 0 && tid == 0) *a.hdr = LinearHdr{total, 0};
+  if (warp == 0) {
+    const int n = n0 + lane;
+    const bool in = n < a.N;
+    const bool on = in && row_active(a, n, &st);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on);
+    const int at = before + __popc(mask & ((1u << lane) - 1u));
+    place[lane] = on ? at : -1;
+    if (on) {
+      a.index[at] = n;
+      a.target[at] = a.targets[n];
+      if (a.scale) {
+        a.scale[at] = a.row_scale ? a.row_scale[n] : 1.f;
+        a.lse_c[at] = a.lse[n];
+        if (a.status) a.status[n] = 0;
+      }
+    } else if (in) {
+      if (a.status) a.status[n] = st;
+      if (a.loss) {
+        const float v = st ? __int_as_float(0x7FC00000) : 0.f;
+        a.loss[n] = v;
+        a.lse_out[n] = v;
+      }
+    }
+  }
+  __syncthreads();
+  const int vecs = a.D / 8;
+  for (int i = warp; i < kPrepRows && n0 + i < a.N; i += kRowWarps) {
+    const int at = place[i];
+    if (at >= 0) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.hidden.base) +
+          row_offset(a.hidden.batch_stride, a.hidden.row_stride, a.hidden.rows_per_batch, n0 + i));
+      uint4* dst = reinterpret_cast<uint4*>(a.h + static_cast<size_t>(at) * a.D);
+      for (int v = lane; v < vecs; v += 32) dst[v] = src[v];
+    } else if (a.grad_hidden) {
+      uint4* dst = reinterpret_cast<uint4*>(a.grad_hidden + static_cast<size_t>(n0 + i) * a.D);
+      for (int v = lane; v < vecs; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  // zero rows behind the last active one: they are read as k rows of dW
+  const int end = (max(total, 1) + a.tile_m - 1) / a.tile_m * a.tile_m;
+  for (int r = total + static_cast<int>(blockIdx.x) * kRowWarps + warp; r < end; r += static_cast<int>(gridDim.x) * kRowWarps) {
+    uint4* dst = reinterpret_cast<uint4*>(a.h + static_cast<size_t>(r) * a.D);
+    for (int v = lane; v < vecs; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+constexpr int kJoinThreads = 1024;  // 32 rows of 32 warps
+
+// Joins the vocabulary tiles' maxima and sums: a lane per row, the warps share
+// the tiles, in a fixed order.
+__global__ void __launch_bounds__(kJoinThreads)
+    ssd_linear_join_kernel(const LinearHdr* hdr, const float2* part, int rows, int tiles, const int32_t* index,
+                           const float* zt, float* loss, float* lse, int32_t* status) {
+  __shared__ float maxima[32][33];
+  __shared__ double sums[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = static_cast<int>(blockIdx.x) * 32 + lane;
+  const int n_active = hdr->n_active;
+  if (static_cast<int>(blockIdx.x) * 32 >= n_active) return;
+  const bool live = row < n_active;
+  float mx = -INFINITY;
+  double sum = 0.0;
+  if (live) {
+#pragma unroll 4
+    for (int t = warp; t < tiles; t += 32) {
+      const float2 p = part[static_cast<size_t>(t) * rows + row];
+      const float m = fmaxf(mx, p.x);
+      const float ref = m > -INFINITY ? m : 0.f;
+      sum = sum * static_cast<double>(ex2((mx - ref) * kLog2e)) +
+            static_cast<double>(p.y) * static_cast<double>(ex2((p.x - ref) * kLog2e));
+      mx = m;
+    }
+  }
+  maxima[warp][lane] = mx;
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && live) {
+    float m = -INFINITY;
+    for (int w = 0; w < 32; ++w) m = fmaxf(m, maxima[w][lane]);
+    const float ref = m > -INFINITY ? m : 0.f;
+    double s = 0.0;
+    for (int w = 0; w < 32; ++w) s += sums[w][lane] * static_cast<double>(ex2((maxima[w][lane] - ref) * kLog2e));
+    const double l = static_cast<double>(ref) + log(s);
+    const int n = index[row];
+    const double z = static_cast<double>(zt[row]);
+    int32_t st = 0;
+    if (!(fabs(l) < INFINITY) || !(fabs(z) < INFINITY)) st |= SSD_ROW_NONFINITE;
+    if (hdr->error) st |= SSD_ROW_DEVICE_TIMEOUT;
+    const float nan = __int_as_float(0x7FC00000);
+    loss[n] = st ? nan : static_cast<float>(l - z);
+    lse[n] = st ? nan : static_cast<float>(l);
+    status[n] = st;
+  }
+}
+
+// Sums dh's slots in order, rounds once, and puts the rows in their places.
+__global__ void __launch_bounds__(128)
+    ssd_linear_dh_kernel(const LinearHdr* hdr, const float* part, int rows, int slots, int D, const int32_t* index,
+                         uint16_t* grad_hidden, int32_t* status) {
+  const int r = static_cast<int>(blockIdx.x);
+  if (r >= hdr->n_active) return;
+  const int n = index[r];
+  const bool bad = hdr->error != 0;
+  if (bad && status && threadIdx.x == 0) status[n] = SSD_ROW_DEVICE_TIMEOUT;
+  for (int d = static_cast<int>(threadIdx.x) * 4; d < D; d += 128 * 4) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < slots; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (static_cast<size_t>(k) * rows + r) * D + d);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    if (bad) s.x = s.y = s.z = s.w = __int_as_float(0x7FC00000);
+    *reinterpret_cast<uint2*>(grad_hidden + static_cast<size_t>(n) * D + d) =
+        make_uint2(Elem<uint16_t>::pack2(s.x, s.y), Elem<uint16_t>::pack2(s.z, s.w));
+  }
+}
+
+}  // namespace ssd

@@ -1,5 +1,6 @@
 // ssd_train.cu -- host side of the draft-training calls of include/ssd.h:
-// ssd_teacher_top, ssd_distill (ssd_rows.cuh).
+// ssd_teacher_top, ssd_distill (ssd_rows.cuh), ssd_linear_ce and
+// ssd_linear_ce_grad (ssd_linear.cuh).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -10,6 +11,7 @@
 
 #include "../../include/ssd.h"
 #include "ssd_device.cuh"
+#include "ssd_linear.cuh"
 #include "ssd_rows.cuh"
 
 namespace ssd {
@@ -91,6 +93,210 @@ static ssd_status check_rows(int dtype, int n_batch, int rows_per_batch, int V, 
 
 static bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// ---------------------------------------------------------------------------
+// The linear head.
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once (libcuda is not linked).
+static EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A row-major [rows, cols] matrix copied in boxes of 128-byte rows, swizzled.
+static bool tile_map(CUtensorMap* m, const void* base, bool fp32, long long cols, long long rows, long long row_bytes,
+                     int box_rows) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {fp32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t step[2] = {1u, 1u};
+  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+            dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSmCount = 148;
+constexpr long long kPieceBytes = 128ll << 20;  // of the gradient's logits, kept at a time
+constexpr int kMaxSlots = 32;
+
+// Sizes of one call, and where its workspace holds what.
+struct LinearPlan {
+  int cg;            // CTAs of one product tile
+  int rows;          // N rounded up to whole tiles
+  int tiles;         // vocabulary tiles of the forward call
+  int piece;         // vocabulary of one piece of the gradient
+  int slots;         // splits of a piece's k axis in dh
+  size_t hdr, index, target, scale, lse, zt, h, part, g, dh, total;
+};
+
+static LinearPlan linear_plan(int N, int D, int V, bool grad) {
+  LinearPlan p = {};
+  p.cg = 1;
+  const int tm = 128 * p.cg;
+  p.rows = (N + tm - 1) / tm * tm;
+  p.tiles = (V + kTileN - 1) / kTileN;
+  const long long v_up = static_cast<long long>(p.tiles) * kTileN;
+  const long long fit = kPieceBytes / (2ll * p.rows) / kTileN * kTileN;
+  p.piece = static_cast<int>(fit < kTileN ? kTileN : (fit > v_up ? v_up : fit));
+  // enough splits to fill the GPU, each of at least 8 blocks of k
+  const int m_tiles = p.rows / tm, d_tiles = (D + kTileN - 1) / kTileN;
+  const int want = (kSmCount / p.cg + m_tiles * d_tiles - 1) / (m_tiles * d_tiles);
+  const int blocks = ((V < p.piece ? V : p.piece) + kBlockK - 1) / kBlockK;
+  const int most = blocks / 8 < 1 ? 1 : (blocks / 8 > kMaxSlots ? kMaxSlots : blocks / 8);
+  p.slots = want < most ? want : most;
+  size_t off = 0;
+  const auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t r = static_cast<size_t>(p.rows);
+  p.hdr = take(sizeof(LinearHdr));
+  p.index = take(r * 4);
+  p.target = take(r * 4);
+  p.h = take(r * static_cast<size_t>(D) * 2);
+  if (grad) {
+    p.scale = take(r * 4);
+    p.lse = take(r * 4);
+    p.g = take(r * static_cast<size_t>(p.piece) * 2);
+    p.dh = take(r * static_cast<size_t>(p.slots) * static_cast<size_t>(D) * 4);
+  } else {
+    p.zt = take(r * 4);
+    p.part = take(r * static_cast<size_t>(p.tiles) * 8);
+  }
+  p.total = off;
+  return p;
+}
+
+template <int Op, int CG>
+static ssd_status launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a,
+                              long long most_tiles, cudaStream_t stream) {
+  const auto fn = &ssd_gemm_kernel<Op, CG>;
+  if (allow_smem(reinterpret_cast<const void*>(fn), GemmShape<CG>::kSmem) != cudaSuccess) return SSD_ERR_CUDA;
+  const long long fit = kSmCount / CG;
+  const long long groups = most_tiles < fit ? most_tiles : fit;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = GemmShape<CG>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+static ssd_status check_linear(int dtype, int n_batch, int rows_per_batch, int D, int V, int64_t batch_stride,
+                               int64_t row_stride, int64_t weight_stride) {
+  if (dtype != SSD_DTYPE_BF16) return SSD_ERR_DTYPE;
+  if (n_batch < 0 || rows_per_batch < 0 || D < 8 || D % 8 != 0 || D > SSD_MAX_LINEAR_D || V < 1 ||
+      V > SSD_MAX_LINEAR_V)
+    return SSD_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_batch) * rows_per_batch > SSD_MAX_LINEAR_N) return SSD_ERR_INVALID_ARG;
+  if (batch_stride < 0 || row_stride < 0 || batch_stride % 8 != 0 || row_stride % 8 != 0) return SSD_ERR_INVALID_ARG;
+  if (weight_stride < D || weight_stride % 8 != 0 || weight_stride >= (1ll << 38)) return SSD_ERR_INVALID_ARG;
+  return SSD_OK;
+}
+
+static void prep_args(PrepArgs* a, const LinearPlan& p, char* ws, const RowsIn& hidden, const int32_t* targets, int N,
+                      int V, int D) {
+  *a = PrepArgs{};
+  a->hdr = reinterpret_cast<LinearHdr*>(ws + p.hdr);
+  a->hidden = hidden;
+  a->targets = targets;
+  a->index = reinterpret_cast<int32_t*>(ws + p.index);
+  a->target = reinterpret_cast<int32_t*>(ws + p.target);
+  a->h = reinterpret_cast<uint16_t*>(ws + p.h);
+  a->N = N;
+  a->V = V;
+  a->D = D;
+  a->tile_m = 128 * p.cg;
+}
+
+static GemmArgs gemm_args(const LinearPlan& p, char* ws, int V, int D) {
+  GemmArgs g = {};
+  g.hdr = reinterpret_cast<const LinearHdr*>(ws + p.hdr);
+  g.error = &reinterpret_cast<LinearHdr*>(ws + p.hdr)->error;
+  g.target = reinterpret_cast<const int32_t*>(ws + p.target);
+  g.rows = p.rows;
+  g.V = V;
+  g.D = D;
+  return g;
+}
+
+template <int CG>
+static ssd_status linear_forward(const LinearPlan& p, char* ws, const void* weight, long long ws_bytes_row, int N, int D,
+                                 int V, float* loss, float* lse, int32_t* status, cudaStream_t stream) {
+  CUtensorMap mh, mw;
+  if (!tile_map(&mh, ws + p.h, false, D, p.rows, 2ll * D, 128) ||
+      !tile_map(&mw, weight, false, D, V, ws_bytes_row, GemmShape<CG>::kBRows))
+    return SSD_ERR_CUDA;
+  GemmArgs g = gemm_args(p, ws, V, D);
+  g.v_count = V;
+  g.zt = reinterpret_cast<float*>(ws + p.zt);
+  g.part = reinterpret_cast<float2*>(ws + p.part);
+  const long long most = static_cast<long long>(p.rows / (128 * CG)) * p.tiles;
+  const ssd_status st = launch_gemm<kOpLse, CG>(mh, mw, mw, g, most, stream);
+  if (st != SSD_OK) return st;
+  ssd_linear_join_kernel<<<(N + 31) / 32, kJoinThreads, 0, stream>>>(
+      g.hdr, g.part, p.rows, p.tiles, reinterpret_cast<const int32_t*>(ws + p.index), g.zt, loss, lse, status);
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+template <int CG>
+static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* weight, long long ws_bytes_row, int N,
+                                  int D, int V, void* grad_hidden, void* grad_weight, int32_t* status,
+                                  cudaStream_t stream) {
+  using S = GemmShape<CG>;
+  CUtensorMap h_k, h_mn, w_k, w_mn, g_out, g_k, g_mn, dh_out, dw_out;
+  if (!tile_map(&h_k, ws + p.h, false, D, p.rows, 2ll * D, 128) ||
+      !tile_map(&h_mn, ws + p.h, false, D, p.rows, 2ll * D, 64) ||
+      !tile_map(&w_k, weight, false, D, V, ws_bytes_row, S::kBRows) ||
+      !tile_map(&w_mn, weight, false, D, V, ws_bytes_row, 64) ||
+      !tile_map(&g_out, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 32) ||
+      !tile_map(&g_k, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 128) ||
+      !tile_map(&g_mn, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 64) ||
+      !tile_map(&dh_out, ws + p.dh, true, D, static_cast<long long>(p.rows) * p.slots, 4ll * D, 32) ||
+      !tile_map(&dw_out, grad_weight, false, D, V, 2ll * D, 32))
+    return SSD_ERR_CUDA;
+  GemmArgs g = gemm_args(p, ws, V, D);
+  g.scale = reinterpret_cast<const float*>(ws + p.scale);
+  g.lse = reinterpret_cast<const float*>(ws + p.lse);
+  g.slots = p.slots;
+  const long long m_tiles = p.rows / S::kTileM, d_tiles = (D + kTileN - 1) / kTileN;
+  for (long long v0 = 0; v0 < V; v0 += p.piece) {
+    g.v0 = static_cast<int>(v0);
+    g.v_count = static_cast<int>(V - v0 < p.piece ? V - v0 : p.piece);
+    g.first = v0 == 0;
+    const long long v_tiles = (g.v_count + kTileN - 1) / kTileN;
+    ssd_status st = launch_gemm<kOpGrad, CG>(h_k, w_k, g_out, g, m_tiles * v_tiles, stream);
+    if (st == SSD_OK) st = launch_gemm<kOpDh, CG>(g_k, w_mn, dh_out, g, m_tiles * d_tiles * p.slots, stream);
+    if (st == SSD_OK)
+      st = launch_gemm<kOpDw, CG>(g_mn, h_mn, dw_out, g, (g.v_count + S::kTileM - 1) / S::kTileM * d_tiles, stream);
+    if (st != SSD_OK) return st;
+  }
+  ssd_linear_dh_kernel<<<N, 128, 0, stream>>>(g.hdr, reinterpret_cast<const float*>(ws + p.dh), p.rows, p.slots, D,
+                                              reinterpret_cast<const int32_t*>(ws + p.index),
+                                              static_cast<uint16_t*>(grad_hidden), status);
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
 }  // namespace ssd
 
 using namespace ssd;
@@ -159,6 +365,68 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == SSD_DTYPE_BF16 ? launch_rows(&ssd_distill_kernel<uint16_t>, a, rows, p, s)
                                  : launch_rows(&ssd_distill_kernel<float>, a, rows, p, s);
+}
+
+size_t ssd_linear_ce_workspace_bytes(int N, int D, int V, int grad) {
+  if (N < 0 || N > SSD_MAX_LINEAR_N || D < 8 || D % 8 != 0 || D > SSD_MAX_LINEAR_D || V < 1 || V > SSD_MAX_LINEAR_V)
+    return 0;
+  return linear_plan(N > 0 ? N : 1, D, V, grad != 0).total;
+}
+
+ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int n_batch, int rows_per_batch, int D,
+                         int V, int64_t batch_stride, int64_t row_stride, int64_t weight_stride,
+                         const int32_t* targets, float* loss, float* lse, int32_t* status, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  ssd_status st = check_linear(dtype, n_batch, rows_per_batch, D, V, batch_stride, row_stride, weight_stride);
+  if (st != SSD_OK) return st;
+  const int N = n_batch * rows_per_batch;
+  if (N == 0) return SSD_OK;
+  if (!hidden || !weight || !targets || !loss || !lse || !status) return SSD_ERR_INVALID_ARG;
+  if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  const LinearPlan p = linear_plan(N, D, V, false);
+  if (!workspace || ws_bytes < p.total) return SSD_ERR_WORKSPACE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  PrepArgs a;
+  prep_args(&a, p, ws, RowsIn{hidden, batch_stride, row_stride, rows_per_batch}, targets, N, V, D);
+  a.loss = loss;
+  a.lse_out = lse;
+  a.status = status;
+  ssd_linear_prep_kernel<<<(N + kPrepRows - 1) / kPrepRows, kRowThreads, 0, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
+  return linear_forward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, loss, lse, status, s);
+}
+
+ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype, int n_batch, int rows_per_batch, int D,
+                              int V, int64_t batch_stride, int64_t row_stride, int64_t weight_stride,
+                              const int32_t* targets, const float* lse, const float* row_scale, void* grad_hidden,
+                              void* grad_weight, int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+  ssd_status st = check_linear(dtype, n_batch, rows_per_batch, D, V, batch_stride, row_stride, weight_stride);
+  if (st != SSD_OK) return st;
+  const int N = n_batch * rows_per_batch;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!grad_weight) return SSD_ERR_INVALID_ARG;
+  if (!aligned_to(grad_weight, 16)) return SSD_ERR_ALIGNMENT;
+  if (N == 0)  // no row: the weight's gradient is zero
+    return cudaMemsetAsync(grad_weight, 0, 2ull * static_cast<size_t>(V) * D, s) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  if (!hidden || !weight || !targets || !lse || !grad_hidden) return SSD_ERR_INVALID_ARG;
+  if (!aligned_to(hidden, 16) || !aligned_to(weight, 16) || !aligned_to(grad_hidden, 16) ||
+      !aligned_to(workspace, 256))
+    return SSD_ERR_ALIGNMENT;
+  const LinearPlan p = linear_plan(N, D, V, true);
+  if (!workspace || ws_bytes < p.total) return SSD_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  PrepArgs a;
+  prep_args(&a, p, ws, RowsIn{hidden, batch_stride, row_stride, rows_per_batch}, targets, N, V, D);
+  a.row_scale = row_scale;
+  a.lse = lse;
+  a.scale = reinterpret_cast<float*>(ws + p.scale);
+  a.lse_c = reinterpret_cast<float*>(ws + p.lse);
+  a.grad_hidden = static_cast<uint16_t*>(grad_hidden);
+  a.status = status;
+  ssd_linear_prep_kernel<<<(N + kPrepRows - 1) / kPrepRows, kRowThreads, 0, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
+  return linear_backward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, grad_hidden, grad_weight, status, s);
 }
 
 }  // extern "C"
