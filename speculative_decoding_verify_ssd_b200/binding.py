@@ -130,7 +130,7 @@ def _check(code: int, what: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -551,10 +551,25 @@ def _rows_of(t: torch.Tensor, name: str):
     return lead[-2], lead[-1], t.shape[-1], strides[-2], strides[-1]
 
 
-def _stream_scope(stream):
-    """`stream`, when one is given, as the stream that the call's own
-    allocations belong to."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+_here = contextlib.nullcontext()
+
+
+class _Scope:
+    """The tensors' device as the current one, and `stream`, when one is given,
+    as the stream that the call's own allocations belong to."""
+
+    def __init__(self, device, stream):
+        self.device = _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = _here if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        self.stream.__exit__(*e)
+        self.device.__exit__(*e)
 
 
 @dataclass
@@ -572,14 +587,14 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
     dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
-    with torch.cuda.device(dev), _stream_scope(stream):
+    with _Scope(dev, stream) as st:
         M = int(M)
         f32 = dict(dtype=torch.float32, device=dev)
         r = TeacherTop(tokens=torch.empty(lead + (max(M, 0),), dtype=torch.int32, device=dev),
                        values=torch.empty(lead + (max(M, 0),), **f32), lse=torch.empty(lead, **f32),
                        tail=torch.empty(lead, **f32), status=torch.empty(lead, dtype=torch.int32, device=dev))
         _check(load().ssd_teacher_top(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(r.tokens),
-                                      _ptr(r.values), _ptr(r.lse), _ptr(r.tail), _ptr(r.status), _stream()),
+                                      _ptr(r.values), _ptr(r.lse), _ptr(r.tail), _ptr(r.status), st),
                "ssd_teacher_top")
     return r
 
@@ -612,7 +627,7 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
             raise ValueError("grad is given but with_grad is False")
         if grad.dtype != logits.dtype or grad.device != dev or grad.shape != logits.shape:
             raise ValueError("grad must have the logits' shape, dtype and device")
-    with torch.cuda.device(dev), _stream_scope(stream):
+    with _Scope(dev, stream) as st:
         if with_grad and grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         gbs, grs = _rows_of(grad, "grad")[3:] if with_grad else (0, 0)
@@ -620,7 +635,7 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
                           status=torch.empty(lead, dtype=torch.int32, device=dev), grad=grad)
         _check(load().ssd_distill(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(tokens), _ptr(values),
                                   _ptr(tail), _ptr(row_scale), _ptr(r.loss), _ptr(r.status), _ptr(grad), gbs, grs,
-                                  _stream()), "ssd_distill")
+                                  st), "ssd_distill")
     return r
 
 
@@ -666,13 +681,13 @@ def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     (negative: left out), without storing the logits (see ssd_linear_ce in
     ssd.h).  hidden [..., D] (up to three dimensions) and weight [V, D] bf16."""
     dev, N, V, args = _linear_args(hidden, weight, targets)
-    with torch.cuda.device(dev), _stream_scope(stream):
+    with _Scope(dev, stream) as st:
         ws = _linear_workspace(workspace, N, hidden.shape[-1], V, False, dev)
         f32 = dict(dtype=torch.float32, device=dev)
         r = LinearCeResult(loss=torch.empty(targets.shape, **f32), lse=torch.empty(targets.shape, **f32),
                            status=torch.empty(targets.shape, dtype=torch.int32, device=dev))
         _check(load().ssd_linear_ce(*args, _ptr(r.loss), _ptr(r.lse), _ptr(r.status), _ptr(ws), ws.numel(),
-                                    _stream()), "ssd_linear_ce")
+                                    st), "ssd_linear_ce")
     return r
 
 
@@ -689,7 +704,7 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
         _need(row_scale, "row_scale", torch.float32, tuple(targets.shape), dev)
     if status is not None:
         _need(status, "status", torch.int32, tuple(targets.shape), dev)
-    with torch.cuda.device(dev), _stream_scope(stream):
+    with _Scope(dev, stream) as st:
         ws = _linear_workspace(workspace, N, D, V, True, dev)
         if grad_hidden is None:
             grad_hidden = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
@@ -698,5 +713,5 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
         _need(grad_hidden, "grad_hidden", torch.bfloat16, tuple(hidden.shape), dev)
         _need(grad_weight, "grad_weight", torch.bfloat16, (V, D), dev)
         _check(load().ssd_linear_ce_grad(*args, _ptr(lse), _ptr(row_scale), _ptr(grad_hidden), _ptr(grad_weight),
-                                         _ptr(status), _ptr(ws), ws.numel(), _stream()), "ssd_linear_ce_grad")
+                                         _ptr(status), _ptr(ws), ws.numel(), st), "ssd_linear_ce_grad")
     return grad_hidden, grad_weight

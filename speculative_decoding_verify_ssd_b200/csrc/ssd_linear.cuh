@@ -41,6 +41,7 @@ struct GemmShape {
 // The head of the workspace.
 struct LinearHdr {
   int32_t n_active, error;
+  float scale_max;  // the largest magnitude among the active rows' scales
 };
 
 struct GemmArgs {
@@ -291,6 +292,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = tmem_base;
   const GemmWait wait = {&abort_flag, a.error};
   const int n_active = a.hdr->n_active;
+  const float scale_max = a.hdr->scale_max;
   const GemmWork<Op, CG> work(a, n_active);
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
 
@@ -467,6 +469,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         } else {
           const int half = c & 1;
           if (tile.n * kTileN + (c >> 1) * 64 < a.D && a.v0 + row0 < a.V) {  // uniform over the warp
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * scale_max);
             if (half == 0) {
               if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
               __syncwarp();
@@ -529,15 +533,14 @@ struct PrepArgs {
   int32_t* target;         // their targets, scales, log-normalisers
   float* scale;
   float* lse_c;
-  uint16_t* h;             // their hidden states, dense, zero rows behind the last up to a tile's end
+  uint16_t* h;             // their hidden states, dense; for the gradient with zero rows up to a whole block of k
   float* loss;             // forward call: what left-out rows get
   float* lse_out;
   uint16_t* grad_hidden;   // gradient call: likewise
   int32_t* status;         // may be NULL in the gradient call
-  int N, V, D, tile_m;
+  int N, V, D;
+  int block_rows;          // rows of one block, at most 32
 };
-
-constexpr int kPrepRows = 32;  // rows of one block
 
 // Whether row n takes part, and its status where it does not.  A row whose
 // log-normaliser is not finite is left out of the gradient: its NaN would reach
@@ -560,22 +563,32 @@ __device__ __forceinline__ bool row_active(const PrepArgs& a, int n, int32_t* st
 
 __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const PrepArgs a) {
   __shared__ int ired[kRowWarps];
-  __shared__ int place[kPrepRows];
+  __shared__ float fred[kRowWarps];
+  __shared__ int place[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n0 = static_cast<int>(blockIdx.x) * kPrepRows;
+  const int n0 = static_cast<int>(blockIdx.x) * a.block_rows;
+  // Every block counts the rows itself: one launch, and 4 bytes a row from L2.
   int before = 0, total = 0;
+  float top = 0.f;
   int32_t st;
   for (int n = tid; n < a.N; n += kRowThreads) {
     const int on = row_active(a, n, &st) ? 1 : 0;
     total += on;
     if (n < n0) before += on;
+    if (on && a.row_scale) top = fmaxf(top, fabsf(a.row_scale[n]));
   }
   before = block_reduce(before, ired, OpAdd());
   total = block_reduce(total, ired, OpAdd());
-  if (blockIdx.x == 0 && tid == 0) *a.hdr = LinearHdr{total, 0};
+  if (a.scale) {
+    // G is formed with each row's share of the largest scale, which itself
+    // multiplies the 32-bit sums: equal scales, the usual case, add no rounding.
+    top = a.row_scale ? block_reduce(top, fred, OpMax()) : 1.f;
+    if (!(top > 0.f && top < INFINITY)) top = 1.f;
+  }
+  if (blockIdx.x == 0 && tid == 0) *a.hdr = LinearHdr{total, 0, top};
   if (warp == 0) {
     const int n = n0 + lane;
-    const bool in = n < a.N;
+    const bool in = lane < a.block_rows && n < a.N;
     const bool on = in && row_active(a, n, &st);
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on);
     const int at = before + __popc(mask & ((1u << lane) - 1u));
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
       a.index[at] = n;
       a.target[at] = a.targets[n];
       if (a.scale) {
-        a.scale[at] = a.row_scale ? a.row_scale[n] : 1.f;
+        a.scale[at] = a.row_scale ? a.row_scale[n] / top : 1.f;
         a.lse_c[at] = a.lse[n];
         if (a.status) a.status[n] = 0;
       }
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
   }
   __syncthreads();
   const int vecs = a.D / 8;
-  for (int i = warp; i < kPrepRows && n0 + i < a.N; i += kRowWarps) {
+  for (int i = warp; i < a.block_rows && n0 + i < a.N; i += kRowWarps) {
     const int at = place[i];
     if (at >= 0) {
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -612,8 +625,9 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
       for (int v = lane; v < vecs; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  // zero rows behind the last active one: they are read as k rows of dW
-  const int end = (max(total, 1) + a.tile_m - 1) / a.tile_m * a.tile_m;
+  if (!a.grad_hidden) return;
+  // zero rows behind the last active one: dW reads whole blocks of k rows
+  const int end = (max(total, 1) + kBlockK - 1) / kBlockK * kBlockK;
   for (int r = total + static_cast<int>(blockIdx.x) * kRowWarps + warp; r < end; r += static_cast<int>(gridDim.x) * kRowWarps) {
     uint4* dst = reinterpret_cast<uint4*>(a.h + static_cast<size_t>(r) * a.D);
     for (int v = lane; v < vecs; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -669,25 +683,29 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-// Sums dh's slots in order, rounds once, and puts the rows in their places.
-__global__ void __launch_bounds__(128)
+constexpr int kDhThreads = 128;
+
+// Sums dh's slots in order, scales and rounds once, and puts the rows in their places.
+__global__ void __launch_bounds__(kDhThreads)
     ssd_linear_dh_kernel(const LinearHdr* hdr, const float* part, int rows, int slots, int D, const int32_t* index,
                          uint16_t* grad_hidden, int32_t* status) {
   const int r = static_cast<int>(blockIdx.x);
-  if (r >= hdr->n_active) return;
+  const int d = (static_cast<int>(blockIdx.y) * kDhThreads + static_cast<int>(threadIdx.x)) * 4;
+  const LinearHdr h = *hdr;
+  if (r >= h.n_active || d >= D) return;
   const int n = index[r];
-  const bool bad = hdr->error != 0;
-  if (bad && status && threadIdx.x == 0) status[n] = SSD_ROW_DEVICE_TIMEOUT;
-  for (int d = static_cast<int>(threadIdx.x) * 4; d < D; d += 128 * 4) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < slots; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (static_cast<size_t>(k) * rows + r) * D + d);
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-    if (bad) s.x = s.y = s.z = s.w = __int_as_float(0x7FC00000);
-    *reinterpret_cast<uint2*>(grad_hidden + static_cast<size_t>(n) * D + d) =
-        make_uint2(Elem<uint16_t>::pack2(s.x, s.y), Elem<uint16_t>::pack2(s.z, s.w));
+  if (h.error && status && d == 0) status[n] = SSD_ROW_DEVICE_TIMEOUT;
+  const float* src = part + static_cast<size_t>(r) * D + d;
+  const size_t step = static_cast<size_t>(rows) * D;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < slots; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(src + k * step);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
+  const float f = h.error ? __int_as_float(0x7FC00000) : h.scale_max;
+  *reinterpret_cast<uint2*>(grad_hidden + static_cast<size_t>(n) * D + d) =
+      make_uint2(Elem<uint16_t>::pack2(s.x * f, s.y * f), Elem<uint16_t>::pack2(s.z * f, s.w * f));
 }
 
 }  // namespace ssd

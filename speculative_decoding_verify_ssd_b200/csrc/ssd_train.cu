@@ -35,7 +35,10 @@ static cudaError_t allow_smem(const void* fn, int bytes) {
 // ---------------------------------------------------------------------------
 // Rows in cluster shared memory.
 // ---------------------------------------------------------------------------
-constexpr long long kSliceTarget = 66 * 1024;  // bytes of a row that one CTA stages: three CTAs fit an SM
+#ifndef SSD_SLICE
+#define SSD_SLICE 66
+#endif
+constexpr long long kSliceTarget = SSD_SLICE * 1024;  // bytes of a row that one CTA stages: three CTAs fit an SM
 constexpr long long kSliceMin = 8 * 1024;      // do not split a row finer than this for the sake of few rows
 constexpr long long kSliceMax = 200 * 1024;
 constexpr int kRowFill = 2 * 148;              // CTAs that fill the GPU
@@ -226,7 +229,18 @@ static void prep_args(PrepArgs* a, const LinearPlan& p, char* ws, const RowsIn& 
   a->N = N;
   a->V = V;
   a->D = D;
-  a->tile_m = 128 * p.cg;
+}
+
+// Few rows per block, so that the copies spread over the GPU; every block
+// reads all targets, so no more than about a thousand blocks.
+static ssd_status launch_prep(PrepArgs& a, cudaStream_t stream) {
+  int rows = (a.N + 1023) / 1024;
+  rows = rows < kRowWarps ? kRowWarps : (rows > 32 ? 32 : rows);
+  a.block_rows = rows;
+  const int blocks = (a.N + rows - 1) / rows;
+  const int zero = a.grad_hidden ? kBlockK / kRowWarps : 1;  // blocks that clear the rows behind the last
+  ssd_linear_prep_kernel<<<blocks < zero ? zero : blocks, kRowThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 static GemmArgs gemm_args(const LinearPlan& p, char* ws, int V, int D) {
@@ -291,9 +305,10 @@ static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* wei
       st = launch_gemm<kOpDw, CG>(g_mn, h_mn, dw_out, g, (g.v_count + S::kTileM - 1) / S::kTileM * d_tiles, stream);
     if (st != SSD_OK) return st;
   }
-  ssd_linear_dh_kernel<<<N, 128, 0, stream>>>(g.hdr, reinterpret_cast<const float*>(ws + p.dh), p.rows, p.slots, D,
-                                              reinterpret_cast<const int32_t*>(ws + p.index),
-                                              static_cast<uint16_t*>(grad_hidden), status);
+  const dim3 grid(static_cast<unsigned>(N), static_cast<unsigned>((D / 4 + kDhThreads - 1) / kDhThreads));
+  ssd_linear_dh_kernel<<<grid, kDhThreads, 0, stream>>>(g.hdr, reinterpret_cast<const float*>(ws + p.dh), p.rows,
+                                                        p.slots, D, reinterpret_cast<const int32_t*>(ws + p.index),
+                                                        static_cast<uint16_t*>(grad_hidden), status);
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -392,8 +407,7 @@ ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int 
   a.loss = loss;
   a.lse_out = lse;
   a.status = status;
-  ssd_linear_prep_kernel<<<(N + kPrepRows - 1) / kPrepRows, kRowThreads, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
+  if ((st = launch_prep(a, s)) != SSD_OK) return st;
   return linear_forward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, loss, lse, status, s);
 }
 
@@ -424,8 +438,7 @@ ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype,
   a.lse_c = reinterpret_cast<float*>(ws + p.lse);
   a.grad_hidden = static_cast<uint16_t*>(grad_hidden);
   a.status = status;
-  ssd_linear_prep_kernel<<<(N + kPrepRows - 1) / kPrepRows, kRowThreads, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
+  if ((st = launch_prep(a, s)) != SSD_OK) return st;
   return linear_backward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, grad_hidden, grad_weight, status, s);
 }
 
