@@ -358,7 +358,8 @@ ssd_status ssd_cache_lookup(const int32_t* offsets, const int32_t* tokens, int B
  * b * rows_per_batch + j.  One cluster of thread blocks stages a whole row in
  * shared memory: rows of up to 1.6 MB (V <= 400000 fp32, 800000 bf16), else
  * SSD_ERR_UNSUPPORTED.  SSD_MIN_TRAIN_T <= T <= SSD_MAX_TRAIN_T.  Results are
- * the same bits on every call.
+ * the same bits on every call with the same inputs at the same alignment
+ * (modulo 16 bytes) and number of rows.
  */
 
 /*

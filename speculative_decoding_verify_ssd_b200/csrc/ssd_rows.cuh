@@ -60,6 +60,10 @@ struct Elem<uint16_t> {
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
+  static __device__ __forceinline__ void unpack2(const uint4& v, f32x2 (&f)[4]) {
+    f[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x)), f[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = f2_pack(bf16_lo(v.z), bf16_hi(v.z)), f[3] = f2_pack(bf16_lo(v.w), bf16_hi(v.w));
+  }
   // the largest element, NaN when any is
   static __device__ __forceinline__ float vec_max(const uint4& v) {
     const uint32_t m = bf16x2_max_nan(bf16x2_max_nan(v.x, v.y), bf16x2_max_nan(v.z, v.w));
@@ -75,6 +79,10 @@ struct Elem<float> {
   static __device__ __forceinline__ float from_float(float f) { return f; }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ void unpack2(const uint4& v, f32x2 (&f)[2]) {
+    f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
@@ -106,18 +114,21 @@ __device__ __forceinline__ Slice slice_of(const TIn* row, int V, int slice_vecs,
 }
 
 // Starts the copies of the slice: whole vectors in bulk (one barrier phase),
-// the row's ragged edge vectors element by element.
+// the row's ragged edge vectors element by element.  One warp; the other
+// threads see the barrier and the edges after the next barrier of the CTA.
 template <typename TIn>
 __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s, uint4* data, uint64_t* bar) {
   constexpr int VE = Elem<TIn>::kVec;
-  const int lo_edge = s.first == 0 && s.head != 0;                         // vector 0 starts before the row
+  const int lane = threadIdx.x & 31;
+  const bool lo_edge = s.count > 0 && s.first == 0 && s.head != 0;  // vector 0 starts before the row
   const int last = (s.head + V + VE - 1) / VE - 1;
-  const int hi_edge = s.first + s.count - 1 == last && (s.head + V) % VE != 0;  // the last one ends behind it
+  const bool hi_edge =  // the last vector ends behind the row
+      s.count > 0 && s.first + s.count - 1 == last && (s.head + V) % VE != 0 && !(lo_edge && s.count == 1);
   const int a = lo_edge ? 1 : 0;
-  int b = s.count - (hi_edge ? 1 : 0);
-  if (s.count == 0) b = 0;
-  const int whole = max(b - a, 0);
-  if (threadIdx.x == 0) {
+  const int whole = max(s.count - a - (hi_edge ? 1 : 0), 0);
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    mbar_init_fence();
     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(whole) * 16u);
     const char* src = reinterpret_cast<const char*>(row) - s.head * static_cast<int>(sizeof(TIn)) +
                       (static_cast<long long>(s.first) + a) * 16;
@@ -128,15 +139,11 @@ __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s
                          static_cast<uint32_t>(min(kPiece, whole - i)) * 16u, bar, policy);
   }
   // at most two edge vectors, VE elements each
-  if (threadIdx.x >= 32 && threadIdx.x < 32 + 2 * VE) {
-    const int e = (threadIdx.x - 32) % VE;
-    const bool second = threadIdx.x >= 32 + VE;
-    const bool mine = s.count > 0 && (second ? hi_edge && !(lo_edge && s.count == 1) : (lo_edge != 0));
-    if (mine) {
-      const int i = second ? s.count - 1 : 0;
-      const int v = (s.first + i) * VE - s.head + e;
-      reinterpret_cast<TIn*>(data + i)[e] = v >= 0 && v < V ? row[v] : Elem<TIn>::neg_inf();
-    }
+  const int e = lane % VE;
+  if (lane < 2 * VE && (lane < VE ? lo_edge : hi_edge)) {
+    const int i = lane < VE ? 0 : s.count - 1;
+    const int v = (s.first + i) * VE - s.head + e;
+    reinterpret_cast<TIn*>(data + i)[e] = v >= 0 && v < V ? row[v] : Elem<TIn>::neg_inf();
   }
 }
 
@@ -181,19 +188,74 @@ struct OpOr {
   __device__ __forceinline__ int operator()(int a, int b) const { return a | b; }
 };
 
-// max + log(sum of exponentials) of two (reference, sum) pairs, natural units:
-// each stands for sum * exp(ref).  A sum of 0 stands for nothing.
+// (reference, sum) stands for sum * exp(reference), natural units; its
+// logarithm.  A sum of 0 stands for nothing.
 __device__ __forceinline__ double lse_of(double ref, double sum) { return sum > 0.0 ? ref + log(sum) : -INFINITY; }
-__device__ __forceinline__ double lse_join(double a, double b) {
-  const double m = fmax(a, b);
-  if (!(m > -INFINITY)) return m;
-  return m + log1p(exp(fmin(a, b) - m));
+
+// The largest of a warp's values, NaN when any is (made the canonical one,
+// whose key is the largest).
+__device__ __forceinline__ float warp_max_nan(float v) {
+  return key_to_float(__reduce_max_sync(0xFFFFFFFFu, ord_key(fmax_nan(v, v))));
+}
+__device__ __forceinline__ double warp_sum_d(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ bool is_number(float v) { return v > -INFINITY && v < INFINITY; }
+
+// The exponentials 2^((f - ref) * c) of a vector's elements, added to `acc`
+// (element pairs apart).  The difference is formed first: scaled logits far
+// from 0 would carry the rounding of c.
+template <typename TIn>
+__device__ __forceinline__ void exp_sum(const uint4& v, f32x2 minus_ref, f32x2 c, f32x2& acc) {
+  f32x2 f[Elem<TIn>::kVec / 2];
+  Elem<TIn>::unpack2(v, f);
+#pragma unroll
+  for (int i = 0; i < Elem<TIn>::kVec / 2; ++i) {
+    float x, y;
+    f2_unpack(f2_mul(f2_add(f[i], minus_ref), c), x, y);
+    acc = f2_add(acc, f2_pack(ex2(x), ex2(y)));
+  }
 }
 
-// What one CTA of a distillation row tells the others.
+// The sum over a thread's vectors of the staged slice.
+template <typename TIn>
+__device__ __forceinline__ float slice_exp_sum(const uint4* data, int count, float ref, float c) {
+  const f32x2 r2 = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
+  f32x2 a0 = 0ull, a1 = 0ull;
+  int i = threadIdx.x;
+  for (; i + kRowThreads < count; i += 2 * kRowThreads) {
+    const uint4 u = data[i], w = data[i + kRowThreads];
+    exp_sum<TIn>(u, r2, c2, a0);
+    exp_sum<TIn>(w, r2, c2, a1);
+  }
+  if (i < count) exp_sum<TIn>(data[i], r2, c2, a0);
+  float x, y;
+  f2_unpack(f2_add(a0, a1), x, y);
+  return x + y;
+}
+
+template <typename TIn>
+__device__ __forceinline__ float slice_max(const uint4* data, int count) {
+  float m = -INFINITY, m1 = -INFINITY;
+  int i = threadIdx.x;
+  for (; i + kRowThreads < count; i += 2 * kRowThreads) {
+    const uint4 u = data[i], w = data[i + kRowThreads];
+    m = fmax_nan(m, Elem<TIn>::vec_max(u));
+    m1 = fmax_nan(m1, Elem<TIn>::vec_max(w));
+  }
+  if (i < count) m = fmax_nan(m, Elem<TIn>::vec_max(data[i]));
+  return fmax_nan(m, m1);
+}
+
+// What one warp of a distillation row tells the cluster: sums of exponentials
+// of its tail logits and atoms around their maxima, sum_m p_m (log p_m - z_m / T)
+// and sum_m p_m.  (The loss takes the sum of the p_m as they were rounded: their
+// errors then enter with the size of log p - log q, not of log q.)
 struct DistillPart {
-  double tail_sum, atom_sum, numer;  // sums of exponentials around the maxima below; sum_m p_m (log p_m - z_m / T)
-  float tail_max, atom_max;
+  double numer, weight;
+  float tail_max, tail_sum, atom_max, atom_sum;
   int flags;
 };
 
@@ -226,23 +288,24 @@ struct DistillArgs {
 //                (q_tail - p_tail) / T * exp(z_v / T) / sum_tail elsewhere.
 // The atoms' logits are taken out of the staged row (replaced by -inf) before
 // the sums, so the tail's sum is formed without them and never by subtraction.
+// Exponentials are 32-bit; log-weights, whose differences the loss is made of,
+// and sums across threads are 64-bit.
 // ---------------------------------------------------------------------------
 template <typename TIn>
 __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
-  __shared__ int32_t ids[SSD_MAX_TOP];
-  __shared__ double dred[kRowWarps];
-  __shared__ float fred[kRowWarps];
-  __shared__ int ired[kRowWarps];
-  __shared__ DistillPart part;
+  __shared__ __align__(16) int32_t ids[SSD_MAX_TOP];
+  __shared__ DistillPart parts[kRowWarps];
   __shared__ DistillJoin join;
+  __shared__ double norm_s, log_p_tail_s;
+  __shared__ int teacher_flags;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int row = static_cast<int>(blockIdx.x) / C;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TIn* src = static_cast<const TIn*>(a.in.base) +
                    row_offset(a.in.batch_stride, a.in.row_stride, a.in.rows_per_batch, row);
   TIn* dst = a.grad ? static_cast<TIn*>(a.grad) +
@@ -263,151 +326,185 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
     return;
   }
 
-  if (tid == 0) {
-    mbar_init(&bar, 1);
-    mbar_init_fence();
-  }
-  __syncthreads();
-  slice_load(src, a.V, s, data, &bar);
-
-  // The teacher's weights, while the copies are in flight: one atom per thread.
+  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
   const double invT = 1.0 / static_cast<double>(a.T);
+  const float c = static_cast<float>(1.4426950408889634 * invT);
+  const int32_t* tokens = a.tokens + static_cast<long long>(row) * a.M;
+  const float* values = a.values + static_cast<long long>(row) * a.M;
+  // One atom per thread.
+  const int id = tid < a.M ? tokens[tid] : -1;
+  const float t = id >= 0 ? values[tid] : -INFINITY;
+  ids[tid] = id;
   int flags = 0;
-  int id = -1;
-  double log_p = -INFINITY;
-  if (tid < a.M) {
-    id = a.tokens[static_cast<long long>(row) * a.M + tid];
-    const float t = a.values[static_cast<long long>(row) * a.M + tid];
-    ids[tid] = id;
-    if (id >= a.V || id < -1) flags |= SSD_ROW_BAD_TOKEN;
-    if (id >= 0) {
-      if (!(t < INFINITY)) flags |= SSD_ROW_NONFINITE;  // NaN or +inf
-      log_p = static_cast<double>(t) * invT;
+  if (id >= a.V || id < -1) flags |= SSD_ROW_BAD_TOKEN;
+  __syncthreads();
+
+  if (warp == 0) {
+    // The teacher's log-normaliser, while the slice's copies are in flight.
+    const float tail = a.tail ? a.tail[row] : -INFINITY;
+    float v[SSD_MAX_TOP / 32];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < SSD_MAX_TOP / 32; ++i) {
+      v[i] = -INFINITY;
+      if (i * 32 < a.M && ids[i * 32 + lane] >= 0) v[i] = values[i * 32 + lane];
+      top = fmax_nan(top, v[i]);
+    }
+    top = warp_max_nan(top);
+    int f = 0;
+    if (!(top < INFINITY) || !(tail < INFINITY)) f = SSD_ROW_NONFINITE;  // NaN or +inf
+    if (!(top > -INFINITY) && !(tail > -INFINITY)) f = SSD_ROW_NONFINITE;  // a teacher without any mass
+    const double at_top = fmax(static_cast<double>(top) * invT, static_cast<double>(tail));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < SSD_MAX_TOP / 32; ++i)
+      if (i * 32 < a.M) sum += ex2(static_cast<float>((static_cast<double>(v[i]) * invT - at_top) * 1.4426950408889634));
+    double total = warp_sum_d(static_cast<double>(sum));
+    if (lane == 0) {
+      total += static_cast<double>(ex2(static_cast<float>((static_cast<double>(tail) - at_top) * 1.4426950408889634)));
+      const double norm = at_top + log(total);
+      norm_s = norm;
+      log_p_tail_s = static_cast<double>(tail) - norm;
+      teacher_flags = f;
     }
   }
-  double log_p_tail = a.tail ? static_cast<double>(a.tail[row]) : -INFINITY;
-  if (!(log_p_tail < INFINITY)) flags |= SSD_ROW_NONFINITE;
-  {
-    const double top = fmax(block_reduce(log_p, dred, OpMax()), log_p_tail);  // the barriers also publish ids
-    if (!(top > -INFINITY)) flags |= SSD_ROW_NONFINITE;                      // a teacher without any mass
-    const double sum = block_reduce(log_p > -INFINITY ? exp(log_p - top) : 0.0, dred, OpAdd()) +
-                       (log_p_tail > -INFINITY ? exp(log_p_tail - top) : 0.0);
-    const double norm = top + log(sum);
-    log_p -= norm;
-    log_p_tail -= norm;
+  if (id >= 0) {  // the same token twice?
+    for (int j = 0; j < tid; j += 4) {
+      const int4 q = *reinterpret_cast<const int4*>(ids + j);
+      if (q.x == id || (q.y == id && j + 1 < tid) || (q.z == id && j + 2 < tid) || (q.w == id && j + 3 < tid))
+        flags |= SSD_ROW_BAD_TOKEN;
+    }
   }
-  const double p = log_p > -INFINITY ? exp(log_p) : 0.0;
-  const double p_tail = log_p_tail > -INFINITY ? exp(log_p_tail) : 0.0;
-  if (id >= 0)
-    for (int j = 0; j < tid; ++j)
-      if (ids[j] == id) flags |= SSD_ROW_BAD_TOKEN;  // the same token twice
-
   flags |= slice_wait(&bar);
-  __syncthreads();  // the edge elements are staged
 
   // Take this slice's atoms out of the staged row.
   const bool mine = id >= v0 && id < v1;
   float z_atom = -INFINITY;
-  flags = block_reduce(flags, ired, OpOr());
-  if (mine && flags == 0) {
+  if (mine) {
     TIn* at = reinterpret_cast<TIn*>(data) + (id + s.head - s.first * VE);
     z_atom = Elem<TIn>::to_float(*at);
     *at = Elem<TIn>::neg_inf();
   }
   __syncthreads();
 
-  const float c = static_cast<float>(1.4426950408889634 * invT);
-  float m = -INFINITY;
-  for (int i = tid; i < s.count; i += kRowThreads) m = fmax_nan(m, Elem<TIn>::vec_max(data[i]));
-  m = block_reduce(m, fred, OpMaxNan());
-  float za_max = block_reduce(mine ? z_atom : -INFINITY, fred, OpMaxNan());
-  if (!(m < INFINITY) || !(za_max < INFINITY)) flags |= SSD_ROW_NONFINITE;
-  const float ref = m > -INFINITY && m < INFINITY ? m : 0.f;
-  float sum = 0.f;
-  for (int i = tid; i < s.count; i += kRowThreads) {
-    float f[VE];
-    Elem<TIn>::unpack(data[i], f);
-#pragma unroll
-    for (int e = 0; e < VE; ++e) sum += ex2((f[e] - ref) * c);
+  const double log_p = static_cast<double>(t) * invT - norm_s;
+  const float p = ex2(static_cast<float>(log_p * 1.4426950408889634));
+  {
+    const float m = warp_max_nan(slice_max<TIn>(data, s.count));
+    if (!(m < INFINITY)) flags |= SSD_ROW_NONFINITE;
+    const float ref = is_number(m) ? m : 0.f;
+    const float sum = warp_sum(slice_exp_sum<TIn>(data, s.count, ref, c));
+    float am = -INFINITY, as = 0.f;
+    double num = 0.0, weight = 0.0;
+    if (warp * 32 < a.M) {
+      am = warp_max_nan(z_atom);
+      if (!(am < INFINITY)) flags |= SSD_ROW_NONFINITE;
+      if (!is_number(am)) am = 0.f;
+      as = warp_sum(ex2((z_atom - am) * c));
+      weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
+      num = warp_sum_d(mine && p > 0.f ? static_cast<double>(p) * (log_p - static_cast<double>(z_atom) * invT) : 0.0);
+    }
+    flags = __reduce_or_sync(0xFFFFFFFFu, flags);
+    if (lane == 0) parts[warp] = DistillPart{num, weight, ref, sum, am, as, flags | teacher_flags};
   }
-  const double tail_sum = block_reduce(static_cast<double>(sum), dred, OpAdd());
-  const float za_ref = za_max > -INFINITY && za_max < INFINITY ? za_max : 0.f;
-  const double atom_sum = block_reduce(
-      z_atom > -INFINITY ? exp((static_cast<double>(z_atom) - static_cast<double>(za_ref)) * invT) : 0.0, dred, OpAdd());
-  const double numer =
-      block_reduce(mine && p > 0.0 ? p * (log_p - static_cast<double>(z_atom) * invT) : 0.0, dred, OpAdd());
-  if (tid == 0) part = DistillPart{tail_sum, atom_sum, numer, ref, za_ref, flags};
   cluster.sync();
 
-  // One warp of every CTA joins the parts, a lane each, in the same order, so
-  // all hold the same bits.
+  // One warp of every CTA joins the warps' parts, at most two per lane, in the
+  // same order, so all hold the same bits.
   const double w = static_cast<double>(scale) * invT;
-  if (tid < 32) {
-    DistillPart q = {0.0, 0.0, 0.0, 0.f, 0.f, 0};
-    if (tid < C) q = *cluster.map_shared_rank(&part, tid);
-    double tail_max = q.tail_sum > 0.0 ? static_cast<double>(q.tail_max) : -INFINITY;
-    double atom_max = q.atom_sum > 0.0 ? static_cast<double>(q.atom_max) : -INFINITY;
-    int fl = q.flags;
+  if (warp == 0) {
+    DistillPart q[2];
 #pragma unroll
-    for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
-      tail_max = fmax(tail_max, __shfl_xor_sync(0xFFFFFFFFu, tail_max, o));
-      atom_max = fmax(atom_max, __shfl_xor_sync(0xFFFFFFFFu, atom_max, o));
-      fl |= __shfl_xor_sync(0xFFFFFFFFu, fl, o);
+    for (int i = 0; i < 2; ++i) {
+      q[i] = DistillPart{};
+      const int r = (i * 32 + lane) / kRowWarps;
+      if (r < C) q[i] = cluster.map_shared_rank(&parts[0], r)[lane % kRowWarps];
     }
-    double tail = q.tail_sum > 0.0 ? q.tail_sum * exp((static_cast<double>(q.tail_max) - tail_max) * invT) : 0.0;
-    double atom = q.atom_sum > 0.0 ? q.atom_sum * exp((static_cast<double>(q.atom_max) - atom_max) * invT) : 0.0;
-    double num = q.numer;
+    float tail_max = -INFINITY, atom_max = -INFINITY;
 #pragma unroll
-    for (int o = kMaxRowCluster / 2; o > 0; o >>= 1) {
-      tail += __shfl_xor_sync(0xFFFFFFFFu, tail, o);
-      atom += __shfl_xor_sync(0xFFFFFFFFu, atom, o);
-      num += __shfl_xor_sync(0xFFFFFFFFu, num, o);
+    for (int i = 0; i < 2; ++i) {
+      if (q[i].tail_sum > 0.f) tail_max = fmaxf(tail_max, q[i].tail_max);
+      if (q[i].atom_sum > 0.f) atom_max = fmaxf(atom_max, q[i].atom_max);
     }
-    if (tid == 0) {
-      const double lse_tail = lse_of(tail_max * invT, tail);
-      const double lse = lse_join(lse_tail, lse_of(atom_max * invT, atom));
-      if (!(lse > -INFINITY)) fl |= SSD_ROW_NONFINITE;  // every logit is -inf
+    tail_max = warp_max_nan(tail_max);
+    atom_max = warp_max_nan(atom_max);
+    int fl = __reduce_or_sync(0xFFFFFFFFu, q[0].flags | q[1].flags);
+    double tail = 0.0, atom = 0.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (q[i].tail_sum > 0.f)
+        tail += static_cast<double>(q[i].tail_sum) * static_cast<double>(ex2((q[i].tail_max - tail_max) * c));
+      if (q[i].atom_sum > 0.f)
+        atom += static_cast<double>(q[i].atom_sum) * static_cast<double>(ex2((q[i].atom_max - atom_max) * c));
+    }
+    tail = warp_sum_d(tail);
+    atom = warp_sum_d(atom);
+    const double num = warp_sum_d(q[0].numer + q[1].numer), weight = warp_sum_d(q[0].weight + q[1].weight);
+    // both around the larger maximum: the smaller one's factor is a true 64-bit
+    // exponential, and the tail's own logarithm is kept where it underflows
+    const double at_top = static_cast<double>(fmaxf(tail_max, atom_max));
+    const float other = tail_max > atom_max ? atom_max : tail_max;
+    const double factor = other > -INFINITY ? exp((static_cast<double>(other) - at_top) * invT) : 0.0;
+    const double total = tail_max > atom_max ? tail + atom * factor : tail * factor + atom;
+    const double logs = log(lane == 0 ? total : tail);  // two logarithms at once
+    const double lse = at_top * invT + __shfl_sync(0xFFFFFFFFu, logs, 0);
+    const double lse_tail = tail > 0.0 ? static_cast<double>(tail_max) * invT + __shfl_sync(0xFFFFFFFFu, logs, 1) : -INFINITY;
+    if (lane == 0) {
+      if (!(total > 0.0)) fl |= SSD_ROW_NONFINITE;  // every logit is -inf
       const bool bad = (fl & SSD_ROW_INVALID) != 0;
+      const double log_p_tail = log_p_tail_s;
+      const double p_tail = static_cast<double>(ex2(static_cast<float>(log_p_tail * 1.4426950408889634)));
       if (rank == 0) {
-        double loss = num + (1.0 - p_tail) * lse;
+        double loss = num + weight * lse;
         if (p_tail > 0.0) loss += p_tail * (log_p_tail - lse_tail + lse);
         if (!bad && !(loss < INFINITY)) fl |= SSD_ROW_ZERO_Q;
         a.loss[row] = bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);
         a.status[row] = fl;
       }
+      const double q_tail = (tail_max > atom_max ? tail : tail * factor) / total;
       join.lse = lse;
-      join.k = bad || !(tail > 0.0) ? 0.f : static_cast<float>(w * (exp(lse_tail - lse) - p_tail) / tail);
-      join.ref = tail > 0.0 ? static_cast<float>(tail_max) : 0.f;
+      join.k = bad || !(tail > 0.0) ? 0.f : static_cast<float>(w * (q_tail - p_tail) / tail);
+      join.ref = tail > 0.0 ? tail_max : 0.f;
       join.bad = bad;
     }
   }
   if (dst) {
     __syncthreads();
     const bool bad = join.bad;
-    const float k = join.k, r0 = join.ref;
+    const f32x2 k2 = f2_pack(join.k, join.k), r2 = f2_pack(-join.ref, -join.ref), c2 = f2_pack(c, c);
     // whole vectors only where the row's places in both tensors agree modulo 16 bytes
     const bool same = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(src)) & 15u) == 0;
+#pragma unroll 2
     for (int i = tid; i < s.count; i += kRowThreads) {
-      float f[VE];
-      Elem<TIn>::unpack(data[i], f);
-      const int v = (s.first + i) * VE - s.head;
+      f32x2 f[VE / 2];
+      float g[VE];
+      Elem<TIn>::unpack2(data[i], f);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) f[e] = bad ? 0.f : k * ex2((f[e] - r0) * c);
+      for (int e = 0; e < VE / 2; ++e) {
+        float x, y;
+        f2_unpack(f2_mul(f2_add(f[e], r2), c2), x, y);
+        f2_unpack(f2_mul(f2_pack(ex2(x), ex2(y)), k2), g[2 * e], g[2 * e + 1]);
+      }
+      if (bad) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) g[e] = 0.f;
+      }
+      const int v = (s.first + i) * VE - s.head;
       if (same && v >= 0 && v + VE <= a.V) {
-        *reinterpret_cast<uint4*>(dst + v) = Elem<TIn>::pack(f);
+        *reinterpret_cast<uint4*>(dst + v) = Elem<TIn>::pack(g);
       } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e)
-          if (v + e >= 0 && v + e < a.V) dst[v + e] = Elem<TIn>::from_float(f[e]);
+          if (v + e >= 0 && v + e < a.V) dst[v + e] = Elem<TIn>::from_float(g[e]);
       }
     }
     __syncthreads();  // the atoms' places are written after the vectors that hold them
     if (mine && !bad) {
-      const double q = z_atom > -INFINITY ? exp(static_cast<double>(z_atom) * invT - join.lse) : 0.0;
-      dst[id] = Elem<TIn>::from_float(static_cast<float>(w * (q - p)));
+      const double q = static_cast<double>(ex2(static_cast<float>((static_cast<double>(z_atom) * invT - join.lse) * 1.4426950408889634)));
+      dst[id] = Elem<TIn>::from_float(static_cast<float>(w * (q - static_cast<double>(p))));
     }
   }
-  cluster.sync();  // no CTA leaves while another may read its part
+  cluster.sync();  // no CTA leaves while another may read its parts
 }
 
 // ---------------------------------------------------------------------------
@@ -424,19 +521,21 @@ struct TopArgs {
   float T;
 };
 
+// What a CTA of a row tells the others.
 struct TopPart {
-  double sum;
-  float max, ref;
-  int count, flags;
+  float sums[kRowWarps];  // of exponentials below the threshold, per warp
+  int count;              // candidates
 };
 
 // Rank 0 gathers the candidates where its slice was staged.
 constexpr int kTopMinBytes = kCandTotal * (sizeof(unsigned long long) + sizeof(float));
 
-// Keys of the cluster's thread maxima, kMaxima / C of them (a power of two)
-// from each CTA: their M-th largest is a lower bound of the row's M-th
-// largest logit, and few logits reach it.
-constexpr int kMaxima = 1024;
+// The row's maxima over groups of threads, kMaxima of them (a lane's group
+// covers 1, 2 or 4 threads): their M-th largest is a lower bound of the row's
+// M-th largest logit, and few logits reach it.
+constexpr int kMaxima = 512;
+static_assert(kMaxima >= 2 * SSD_MAX_TOP, "more maxima than logits asked for");
+constexpr uint32_t kKeyTimeout = 0xFFFFFFFEu;  // stands for a slice that did not arrive; a NaN's key is 0xFFFFFFFF
 
 // The key of a logit from its kKeyBits high bits: the bits below them are the
 // complement of the mantissa's zeros in a negative logit's key.
@@ -446,25 +545,47 @@ __device__ __forceinline__ uint32_t full_key(uint32_t k) {
   return k;
 }
 
+// The 16 high bits of the M-th largest of a warp's keys: two bits a pass, the
+// three counts of a pass (at most kMaxima each) in one word.
+__device__ __forceinline__ uint32_t maxima_threshold(const uint32_t (&keys)[kMaxima / 32], int M) {
+  uint32_t prefix = 0u;
+#pragma unroll
+  for (int bit = 30; bit >= 16; bit -= 2) {
+    const uint32_t c1 = prefix | (1u << bit), c2 = prefix | (2u << bit), c3 = prefix | (3u << bit);
+    uint32_t n = 0u;
+#pragma unroll
+    for (int i = 0; i < kMaxima / 32; ++i)
+      n += (keys[i] >= c1 ? 1u : 0u) + (keys[i] >= c2 ? 1u << 10 : 0u) + (keys[i] >= c3 ? 1u << 20 : 0u);
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    const int n1 = n & 1023u, n2 = (n >> 10) & 1023u, n3 = n >> 20;
+    prefix = n3 >= M ? c3 : (n2 >= M ? c2 : (n1 >= M ? c1 : prefix));
+  }
+  return prefix;
+}
+
 template <typename TIn>
 __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
   __shared__ uint32_t maxima[kRowThreads];
+  __shared__ uint32_t all_maxima[kMaxima];
   __shared__ unsigned long long cand[kCandPerCta];
   __shared__ double dred[kRowWarps];
   __shared__ float fred[kRowWarps];
   __shared__ int ired[kRowWarps];
   __shared__ int counts[4];  // per-CTA counts exchanged by the exact select
-  __shared__ int n_cand;
-  __shared__ uint32_t tau_s;
-  __shared__ TopPart part, part2;
+  __shared__ double far_sum;
+  __shared__ float far_max;
+  __shared__ int n_cand, total_s;
+  __shared__ double below_s;
+  __shared__ uint32_t tau_s, row_key_s;
+  __shared__ TopPart part;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
   const int row = static_cast<int>(blockIdx.x) / C;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TIn* src = static_cast<const TIn*>(a.in.base) +
                    row_offset(a.in.batch_stride, a.in.row_stride, a.in.rows_per_batch, row);
   const Slice s = slice_of(src, a.V, a.slice_vecs, rank);
@@ -472,34 +593,46 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
   const double invT = 1.0 / static_cast<double>(a.T);
   const float c = static_cast<float>(1.4426950408889634 * invT);
 
-  if (tid == 0) {
-    mbar_init(&bar, 1);
-    mbar_init_fence();
-    n_cand = 0;
+  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
+  if (tid == 0) n_cand = 0;
+  __syncthreads();
+  const bool here = slice_wait(&bar) == 0;
+  {
+    uint32_t k = here ? ord_key(slice_max<TIn>(data, s.count)) : kKeyTimeout;
+    if (C > 2) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+    if (C > 4) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
+    maxima[tid] = k;
   }
-  __syncthreads();
-  slice_load(src, a.V, s, data, &bar);
-  int flags = slice_wait(&bar);
-  __syncthreads();
-
-  float m = -INFINITY;
-  for (int i = tid; i < s.count; i += kRowThreads) m = fmax_nan(m, Elem<TIn>::vec_max(data[i]));
-  maxima[tid] = ord_key(m);
-  m = block_reduce(m, fred, OpMaxNan());
-  flags = block_reduce(flags, ired, OpOr());
-  if (!(m < INFINITY)) flags |= SSD_ROW_NONFINITE;
-  if (tid == 0) part = TopPart{0.0, m, 0.f, 0, flags};
   cluster.sync();
 
-  int fl = 0;
-  float row_max = -INFINITY;
-  for (int r = 0; r < C; ++r) {
-    const TopPart* q = cluster.map_shared_rank(&part, r);
-    fl |= q->flags;
-    row_max = fmax_nan(row_max, q->max);
+  // The threshold tau.
+  {
+    const int shift = C <= 2 ? 0 : (C <= 4 ? 1 : 2);  // every (1 << shift)-th entry of a CTA's maxima counts
+    const int per = kRowThreads >> shift;
+#pragma unroll
+    for (int i = 0; i < kMaxima / kRowThreads; ++i) {
+      const int k = i * kRowThreads + tid, r = k / per;
+      all_maxima[k] = r < C ? cluster.map_shared_rank(&maxima[0], r)[(k % per) << shift] : 0u;
+    }
   }
-  if (!(row_max > -INFINITY)) fl |= SSD_ROW_NONFINITE;
-  if (fl) {
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t keys[kMaxima / 32], top = 0u;
+#pragma unroll
+    for (int i = 0; i < kMaxima / 32; ++i) {
+      keys[i] = all_maxima[i * 32 + lane];
+      top = max(top, keys[i]);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const uint32_t t = maxima_threshold(keys, a.M);
+    if (lane == 0) {
+      tau_s = t;
+      row_key_s = top;
+    }
+  }
+  __syncthreads();
+  const uint32_t row_key = row_key_s;
+  if (row_key >= ord_key(INFINITY) || row_key <= ord_key(-INFINITY)) {  // the same in every CTA
     if (rank == 0) {
       for (int i = tid; i < a.M; i += kRowThreads) {
         a.tokens[static_cast<long long>(row) * a.M + i] = -1;
@@ -507,75 +640,77 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
       }
       if (tid == 0) {
         a.lse[row] = a.tail[row] = __int_as_float(0x7FC00000);
-        a.status[row] = fl;
+        a.status[row] = row_key == kKeyTimeout ? SSD_ROW_DEVICE_TIMEOUT : SSD_ROW_NONFINITE;
       }
     }
-    cluster.sync();
+    cluster.sync();  // no CTA leaves while another may read its maxima
     return;
   }
-
-  // The threshold tau.
-  if (tid < 32) {
-    uint32_t keys[kMaxima / 32];
-    const int per = C <= 4 ? kRowThreads : kRowThreads / 2;  // maxima taken from each CTA
-#pragma unroll
-    for (int i = 0; i < kMaxima / 32; ++i) {
-      const int k = i * 32 + lane, r = k / per, t = k % per;
-      uint32_t v = 0u;
-      if (r < C) {
-        const uint32_t* q = cluster.map_shared_rank(&maxima[0], r);
-        v = per == kRowThreads ? q[t] : max(q[t], q[t + per]);
-      }
-      keys[i] = v;
-    }
-    const uint32_t t = warp_kth_largest<kMaxima / 32>(keys, a.M, Elem<TIn>::kKeyBits);
-    if (lane == 0) tau_s = t;
-  }
-  __syncthreads();
-  const uint32_t tau_key = tau_s;
+  const float row_max = key_to_float(row_key);
   // With fewer maxima than M, or M of them -inf, every logit is a candidate.
+  // (A threshold cut to 16 bits is below the M-th maximum, or that itself.)
+  const uint32_t tau_key = tau_s;
   const float tau = tau_key <= ord_key(-INFINITY) ? -INFINITY : key_to_float(full_key<TIn>(tau_key));
   const float ref = tau > -INFINITY ? tau : 0.f;
-  float sum = 0.f;
-  for (int i = tid; i < s.count; i += kRowThreads) {
-    const uint4 v = data[i];
-    float f[VE];
-    Elem<TIn>::unpack(v, f);
-    if (Elem<TIn>::vec_max(v) >= tau) {
+  float sum;
+  {
+    const f32x2 r2 = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
+    f32x2 acc = 0ull;
+    float apart = 0.f;
+#pragma unroll 2
+    for (int i = tid; i < s.count; i += kRowThreads) {
+      const uint4 v = data[i];
+      if (Elem<TIn>::vec_max(v) >= tau) {
+        float f[VE];
+        Elem<TIn>::unpack(v, f);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const int id = base + i * VE + e;
-        if (f[e] >= tau) {
-          if (id >= 0 && id < a.V) {
-            const int at = atomicAdd(&n_cand, 1);
-            if (at < kCandPerCta) cand[at] = rank_key(f[e], id);
+        for (int e = 0; e < VE; ++e) {
+          const int id = base + i * VE + e;
+          if (f[e] >= tau) {
+            if (id >= 0 && id < a.V) {
+              const int at = atomicAdd(&n_cand, 1);
+              if (at < kCandPerCta) cand[at] = rank_key(f[e], id);
+            }
+          } else {
+            apart += ex2((f[e] - ref) * c);
           }
-        } else {
-          sum += ex2((f[e] - ref) * c);
         }
+      } else {
+        exp_sum<TIn>(v, r2, c2, acc);
       }
-    } else {
+    }
+    float x, y;
+    f2_unpack(acc, x, y);
+    sum = warp_sum(x + y + apart);
+  }
+  if (lane == 0) part.sums[warp] = sum;
+  __syncthreads();
+  if (tid == 0) part.count = n_cand;
+  cluster.sync();
+  if (warp == 0) {
+    double b = 0.0;
+    int n = 0;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) sum += ex2((f[e] - ref) * c);
+    for (int i = 0; i < 2; ++i) {
+      const int r = (i * 32 + lane) / kRowWarps;
+      if (r < C) {
+        const TopPart* q = cluster.map_shared_rank(&part, r);
+        b += static_cast<double>(q->sums[lane % kRowWarps]);
+        if (lane % kRowWarps == 0) n += q->count > kCandPerCta ? kCandTotal + 1 : q->count;
+      }
+    }
+    b = warp_sum_d(b);
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) {
+      below_s = b;
+      total_s = n;
     }
   }
-  double below = block_reduce(static_cast<double>(sum), dred, OpAdd());
-  if (tid == 0) {
-    part2.sum = below;
-    part2.count = n_cand;
-  }
-  cluster.sync();
-  int total = 0;
-  bool over = false;
-  below = 0.0;
-  for (int r = 0; r < C; ++r) {
-    const TopPart* q = cluster.map_shared_rank(&part2, r);
-    total += q->count;
-    over |= q->count > kCandPerCta;
-    below += q->sum;
-  }
-  over |= total > kCandTotal;
-  double ref_d = static_cast<double>(ref);
+  __syncthreads();
+  double below = below_s;
+  int total = total_s;
+  const bool over = total > kCandTotal;
+  float ref_f = ref;
   float limit = tau;  // the tail's logits are below it (or equal to it and counted apart)
 
   if (over) {
@@ -641,7 +776,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
     eq = block_reduce(eq, ired, OpAdd());
     if (tid == 0) {
       counts[0] = gt, counts[1] = eq;
-      part2.sum = below;
+      far_sum = below;
     }
     cluster.sync();
     int eq_before = 0, eq_all = 0;
@@ -651,7 +786,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
       above += q[0];
       if (r < rank) eq_before += q[1];
       eq_all += q[1];
-      below += cluster.map_shared_rank(&part2, r)->sum;
+      below += *cluster.map_shared_rank(&far_sum, r);
     }
     const int need = a.M - above;  // of the equal ones, in token order
     int taken = eq_before;
@@ -699,8 +834,8 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
       taken += chunk;
     }
     __syncthreads();
-    if (tid == 0) part2.count = n_cand;
-    ref_d = static_cast<double>(kref);
+    if (tid == 0) part.count = n_cand;
+    ref_f = kref;
     limit = kth;
     if (kth > -INFINITY) below += static_cast<double>(eq_all - need);
     cluster.sync();
@@ -718,10 +853,10 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
         if (f[e] < limit) tm = fmaxf(tm, f[e]);
     }
     tm = block_reduce(tm, fred, OpMax());
-    if (tid == 0) part.max = tm;
+    if (tid == 0) far_max = tm;
     cluster.sync();
     tm = -INFINITY;
-    for (int r = 0; r < C; ++r) tm = fmaxf(tm, cluster.map_shared_rank(&part, r)->max);
+    for (int r = 0; r < C; ++r) tm = fmaxf(tm, *cluster.map_shared_rank(&far_max, r));
     sum = 0.f;
     if (tm > -INFINITY)
       for (int i = tid; i < s.count; i += kRowThreads) {
@@ -732,58 +867,64 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
           if (f[e] < limit) sum += ex2((f[e] - tm) * c);
       }
     below = block_reduce(static_cast<double>(sum), dred, OpAdd());
-    if (tid == 0) part2.sum = below;
+    if (tid == 0) far_sum = below;
     cluster.sync();
     below = 0.0;
-    for (int r = 0; r < C; ++r) below += cluster.map_shared_rank(&part2, r)->sum;
-    if (tm > -INFINITY) ref_d = static_cast<double>(tm);
+    for (int r = 0; r < C; ++r) below += *cluster.map_shared_rank(&far_sum, r);
+    if (tm > -INFINITY) ref_f = tm;
   }
 
-  if (rank == 0) {
-    // Gather and rank the candidates; those past the M-th belong to the tail.
-    // The sums run over the ranked order, whatever order the candidates came in.
-    unsigned long long* pool = reinterpret_cast<unsigned long long*>(data);
-    float* ranked = reinterpret_cast<float*>(pool + kCandTotal);
-    __syncthreads();  // the staged logits are no longer read
-    int off = 0;
-    for (int r = 0; r < C; ++r) {
-      const int n = min(cluster.map_shared_rank(&part2, r)->count, kCandPerCta);
-      const unsigned long long* q = cluster.map_shared_rank(&cand[0], r);
-      for (int i = tid; i < n && off + i < kCandTotal; i += kRowThreads) pool[off + i] = q[i];
-      off = min(off + n, kCandTotal);
-    }
-    __syncthreads();
-    for (int i = tid; i < off; i += kRowThreads) {
-      const unsigned long long k = pool[i];
-      int pos = 0;
-      for (int j = 0; j < off; ++j) pos += pool[j] > k;
-      const float z = key_to_float(static_cast<uint32_t>(k >> 32));
-      ranked[pos] = z;
-      if (pos < a.M) {
-        a.tokens[static_cast<long long>(row) * a.M + pos] =
-            static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k & 0xFFFFFFFFull));
-        a.values[static_cast<long long>(row) * a.M + pos] = z;
-      }
-    }
-    __syncthreads();
-    double top_sum = 0.0, rest = 0.0;
-    for (int i = tid; i < off; i += kRowThreads) {
-      const double z = static_cast<double>(ranked[i]);
-      if (i < a.M)
-        top_sum += exp((z - static_cast<double>(row_max)) * invT);
-      else if (z > -INFINITY)
-        rest += exp((z - ref_d) * invT);
-    }
-    top_sum = block_reduce(top_sum, dred, OpAdd());
-    rest = block_reduce(rest, dred, OpAdd());
-    if (tid == 0) {
-      const double t = lse_of(ref_d * invT, below + rest);
-      a.tail[row] = static_cast<float>(t);
-      a.lse[row] = static_cast<float>(lse_join(t, lse_of(static_cast<double>(row_max) * invT, top_sum)));
-      a.status[row] = 0;
+  if (rank != 0) {
+    cluster.sync();  // rank 0 has read this CTA's candidates
+    return;
+  }
+  // Gather and rank the candidates; those past the M-th belong to the tail.
+  // The sums run over the ranked order, whatever order the candidates came in.
+  unsigned long long* pool = reinterpret_cast<unsigned long long*>(data);
+  float* ranked = reinterpret_cast<float*>(pool + kCandTotal);
+  __syncthreads();  // the staged logits are no longer read
+  int off = 0;
+  for (int r = 0; r < C; ++r) {
+    const int n = min(cluster.map_shared_rank(&part, r)->count, kCandPerCta);
+    const unsigned long long* q = cluster.map_shared_rank(&cand[0], r);
+    for (int i = tid; i < n && off + i < kCandTotal; i += kRowThreads) pool[off + i] = q[i];
+    off = min(off + n, kCandTotal);
+  }
+  cluster.sync();
+  for (int i = tid; i < off; i += kRowThreads) {
+    const unsigned long long k = pool[i];
+    int pos = 0;
+#pragma unroll 4
+    for (int j = 0; j < off; ++j) pos += pool[j] > k;
+    const float z = key_to_float(static_cast<uint32_t>(k >> 32));
+    ranked[pos] = z;
+    if (pos < a.M) {
+      a.tokens[static_cast<long long>(row) * a.M + pos] =
+          static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k & 0xFFFFFFFFull));
+      a.values[static_cast<long long>(row) * a.M + pos] = z;
     }
   }
-  cluster.sync();  // rank 0 has read the others' candidates
+  __syncthreads();
+  float top_sum = 0.f, rest = 0.f;
+  for (int i = tid; i < off; i += kRowThreads) {
+    const float z = ranked[i];
+    if (i < a.M)
+      top_sum += ex2((z - row_max) * c);
+    else
+      rest += ex2((z - ref_f) * c);
+  }
+  const double top_d = block_reduce(static_cast<double>(top_sum), dred, OpAdd());
+  const double rest_d = block_reduce(static_cast<double>(rest), dred, OpAdd());
+  if (warp == 0) {
+    const double t = below + rest_d;  // around ref_f
+    const double share = t > 0.0 ? t * exp((static_cast<double>(ref_f) - static_cast<double>(row_max)) * invT) : 0.0;
+    const double logs = log(lane == 0 ? t : top_d + share);  // two logarithms at once
+    if (lane == 0) {
+      a.tail[row] = t > 0.0 ? static_cast<float>(static_cast<double>(ref_f) * invT + logs) : -INFINITY;
+      a.status[row] = 0;
+    }
+    if (lane == 1) a.lse[row] = static_cast<float>(static_cast<double>(row_max) * invT + logs);
+  }
 }
 
 }  // namespace ssd

@@ -36,7 +36,7 @@ static cudaError_t allow_smem(const void* fn, int bytes) {
 // Rows in cluster shared memory.
 // ---------------------------------------------------------------------------
 #ifndef SSD_SLICE
-#define SSD_SLICE 66
+#define SSD_SLICE 52
 #endif
 constexpr long long kSliceTarget = SSD_SLICE * 1024;  // bytes of a row that one CTA stages: three CTAs fit an SM
 constexpr long long kSliceMin = 8 * 1024;      // do not split a row finer than this for the sake of few rows

@@ -187,8 +187,8 @@ def teacher(shape, V, M, T, seed, use_tail, device="cuda"):
 
 def check_distill(logits, tokens, values, tail, T, scale=None, grad=None):
     before = logits.clone()
+    alone = ssd.ssd_distill(logits, tokens, values, tail, T, row_scale=scale, with_grad=False)
     r = ssd.ssd_distill(logits, tokens, values, tail, T, row_scale=scale, grad=grad)
-    alone = ssd.ssd_distill(before, tokens, values, tail, T, row_scale=scale, with_grad=False)
     torch.cuda.synchronize()
     loss, want, b = distill_ref(before, tokens, values, tail, T, scale)
     if scale is not None:
