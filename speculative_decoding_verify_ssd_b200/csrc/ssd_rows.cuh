@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
   __shared__ __align__(16) int32_t ids[SSD_MAX_TOP];
+  __shared__ float atoms[SSD_MAX_TOP];
   __shared__ DistillPart parts[kRowWarps];
   __shared__ DistillJoin join;
   __shared__ double norm_s, log_p_tail_s;
@@ -311,7 +312,11 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   TIn* dst = a.grad ? static_cast<TIn*>(a.grad) +
                           row_offset(a.g_batch_stride, a.g_row_stride, a.in.rows_per_batch, row)
                     : nullptr;
+  // All of the row's small inputs are asked for at once; one atom per thread.
   const float scale = a.row_scale ? a.row_scale[row] : 1.f;
+  const float tail_in = a.tail ? a.tail[row] : -INFINITY;
+  const int id = tid < a.M ? a.tokens[static_cast<long long>(row) * a.M + tid] : -1;
+  const float t_in = tid < a.M ? a.values[static_cast<long long>(row) * a.M + tid] : -INFINITY;
   const Slice s = slice_of(src, a.V, a.slice_vecs, rank);
   // the first element of the slice, and one past its last
   const int v0 = max(s.first * VE - s.head, 0), v1 = s.count > 0 ? min((s.first + s.count) * VE - s.head, a.V) : v0;
@@ -329,25 +334,21 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
   const double invT = 1.0 / static_cast<double>(a.T);
   const float c = static_cast<float>(1.4426950408889634 * invT);
-  const int32_t* tokens = a.tokens + static_cast<long long>(row) * a.M;
-  const float* values = a.values + static_cast<long long>(row) * a.M;
-  // One atom per thread.
-  const int id = tid < a.M ? tokens[tid] : -1;
-  const float t = id >= 0 ? values[tid] : -INFINITY;
+  const float t = id >= 0 ? t_in : -INFINITY;
   ids[tid] = id;
+  atoms[tid] = t;
   int flags = 0;
   if (id >= a.V || id < -1) flags |= SSD_ROW_BAD_TOKEN;
   __syncthreads();
 
   if (warp == 0) {
     // The teacher's log-normaliser, while the slice's copies are in flight.
-    const float tail = a.tail ? a.tail[row] : -INFINITY;
+    const float tail = tail_in;
     float v[SSD_MAX_TOP / 32];
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < SSD_MAX_TOP / 32; ++i) {
-      v[i] = -INFINITY;
-      if (i * 32 < a.M && ids[i * 32 + lane] >= 0) v[i] = values[i * 32 + lane];
+      v[i] = i * 32 < a.M ? atoms[i * 32 + lane] : -INFINITY;
       top = fmax_nan(top, v[i]);
     }
     top = warp_max_nan(top);
@@ -368,12 +369,16 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
       teacher_flags = f;
     }
   }
-  if (id >= 0) {  // the same token twice?
-    for (int j = 0; j < tid; j += 4) {
+  // Is a token there twice?  The other warps look, while the first is busy.
+  for (int m = tid - 32; m >= 0 && m < a.M; m += kRowThreads - 32) {
+    const int want = ids[m];
+    bool twice = false;
+#pragma unroll 4
+    for (int j = 0; j < m; j += 4) {
       const int4 q = *reinterpret_cast<const int4*>(ids + j);
-      if (q.x == id || (q.y == id && j + 1 < tid) || (q.z == id && j + 2 < tid) || (q.w == id && j + 3 < tid))
-        flags |= SSD_ROW_BAD_TOKEN;
+      twice |= q.x == want || (q.y == want && j + 1 < m) || (q.z == want && j + 2 < m) || (q.w == want && j + 3 < m);
     }
+    if (twice && want >= 0) flags |= SSD_ROW_BAD_TOKEN;
   }
   flags |= slice_wait(&bar);
 
@@ -468,8 +473,9 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
       join.bad = bad;
     }
   }
+  __syncthreads();
+  cluster.barrier_arrive();  // this CTA has read the others' parts
   if (dst) {
-    __syncthreads();
     const bool bad = join.bad;
     const f32x2 k2 = f2_pack(join.k, join.k), r2 = f2_pack(-join.ref, -join.ref), c2 = f2_pack(c, c);
     // whole vectors only where the row's places in both tensors agree modulo 16 bytes
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
       dst[id] = Elem<TIn>::from_float(static_cast<float>(w * (q - static_cast<double>(p))));
     }
   }
-  cluster.sync();  // no CTA leaves while another may read its parts
+  cluster.barrier_wait();  // no CTA leaves while another may read its parts
 }
 
 // ---------------------------------------------------------------------------
