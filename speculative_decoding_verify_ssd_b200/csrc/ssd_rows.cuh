@@ -31,6 +31,7 @@ struct RowsIn {
 
 __device__ __forceinline__ long long row_offset(long long batch_stride, long long row_stride, int rows_per_batch,
                                                 int row) {
+  if (rows_per_batch == 0) return row * row_stride;  // one stride reaches every row
   const int b = row / rows_per_batch;
   return b * batch_stride + static_cast<long long>(row - b * rows_per_batch) * row_stride;
 }
@@ -202,6 +203,13 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+// The sum over lanes 0 to 7, in every lane; the other lanes' values do not count.
+template <typename T>
+__device__ __forceinline__ T warp_sum8(T v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
 __device__ __forceinline__ bool is_number(float v) { return v > -INFINITY && v < INFINITY; }
 
 // The exponentials 2^((f - ref) * c) of a vector's elements, added to `acc`
@@ -249,21 +257,77 @@ __device__ __forceinline__ float slice_max(const uint4* data, int count) {
   return fmax_nan(m, m1);
 }
 
-// What one warp of a distillation row tells the cluster: sums of exponentials
-// of its tail logits and atoms around their maxima, sum_m p_m (log p_m - z_m / T)
-// and sum_m p_m.  (The loss takes the sum of the p_m as they were rounded: their
-// errors then enter with the size of log p - log q, not of log q.)
-struct DistillPart {
-  double numer, weight;
+// The gradient outside the atoms, k 2^((f - ref) c), of a staged vector.
+template <typename TIn>
+struct GradOf;
+// Rounded to bf16: |k| goes into the exponent, and where |ref c| is moderate the
+// product f c may carry c's rounding (2^-24 |f c|, below 2^-13).
+template <>
+struct GradOf<uint16_t> {
+  f32x2 c2, d2, r2;
+  uint32_t sign;
+  bool far;
+  __device__ __forceinline__ GradOf(float k, float ref, float c) {
+    far = !(fabsf(ref * c) <= 1024.f);
+    const float d = log2f(fabsf(k)) - (far ? 0.f : ref * c);
+    c2 = f2_pack(c, c);
+    d2 = f2_pack(d, d);
+    r2 = f2_pack(-ref, -ref);
+    sign = k < 0.f ? 0x80008000u : 0u;
+  }
+  __device__ __forceinline__ uint32_t pair(f32x2 f) const {
+    float x, y;
+    f2_unpack(f2_fma(f, c2, d2), x, y);
+    return Elem<uint16_t>::pack2(ex2(x), ex2(y)) ^ sign;
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
+    f32x2 f[4];
+    Elem<uint16_t>::unpack2(v, f);
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = f2_add(f[i], r2);
+    }
+    return make_uint4(pair(f[0]), pair(f[1]), pair(f[2]), pair(f[3]));
+  }
+};
+template <>
+struct GradOf<float> {
+  f32x2 k2, r2, c2;
+  __device__ __forceinline__ GradOf(float k, float ref, float c) {
+    k2 = f2_pack(k, k);
+    r2 = f2_pack(-ref, -ref);
+    c2 = f2_pack(c, c);
+  }
+  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
+    f32x2 f[2];
+    float g[4];
+    Elem<float>::unpack2(v, f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x, y;
+      f2_unpack(f2_mul(f2_add(f[e], r2), c2), x, y);
+      f2_unpack(f2_mul(f2_pack(ex2(x), ex2(y)), k2), g[2 * e], g[2 * e + 1]);
+    }
+    return Elem<float>::pack(g);
+  }
+};
+
+// What one warp, and then one CTA, of a distillation row found: sums of
+// exponentials of its tail logits and atoms around their maxima (tail_sum NaN:
+// the row is void), and for the loss sum_m p_m ((t_m - top) - z_m) / T and sum_m p_m.
+// (The loss takes the sum of the p_m as they were rounded: their errors then
+// enter with the size of log p - log q, not of log q.)
+struct __align__(16) DistillPart {
   float tail_max, tail_sum, atom_max, atom_sum;
+  double numer, weight;
   int flags;
 };
 
-// What the gradient needs of the joined row.
-struct DistillJoin {
-  double lse;
-  float k, ref;  // gradient outside the atoms: k * exp((z - ref) / T)
-  int bad;
+// The teacher's weights: p_m = exp((t_m - top) / T) / total, p_tail likewise.
+struct DistillTeacher {
+  double top, total;  // top in units of logits / T
+  float inv_total, p_tail;
+  int flags;
 };
 
 struct DistillArgs {
@@ -277,7 +341,8 @@ struct DistillArgs {
   void* grad;              // or NULL
   long long g_batch_stride, g_row_stride;
   int V, M, slice_vecs;
-  float T;
+  double inv_t;   // 1 / T
+  float log2e_t;  // log2(e) / T
 };
 
 // ---------------------------------------------------------------------------
@@ -292,16 +357,15 @@ struct DistillArgs {
 // and sums across threads are 64-bit.
 // ---------------------------------------------------------------------------
 template <typename TIn>
-__global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const DistillArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
   __shared__ __align__(16) int32_t ids[SSD_MAX_TOP];
   __shared__ float atoms[SSD_MAX_TOP];
-  __shared__ DistillPart parts[kRowWarps];
-  __shared__ DistillJoin join;
-  __shared__ double norm_s, log_p_tail_s;
-  __shared__ int teacher_flags;
+  __shared__ DistillPart warps[kRowWarps];
+  __shared__ DistillPart parts[kMaxRowCluster];  // the cluster's, written by their CTAs
+  __shared__ DistillTeacher teacher;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
@@ -332,8 +396,8 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   }
 
   if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
-  const double invT = 1.0 / static_cast<double>(a.T);
-  const float c = static_cast<float>(1.4426950408889634 * invT);
+  const double invT = a.inv_t;
+  const float c = a.log2e_t;
   const float t = id >= 0 ? t_in : -INFINITY;
   ids[tid] = id;
   atoms[tid] = t;
@@ -342,8 +406,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   __syncthreads();
 
   if (warp == 0) {
-    // The teacher's log-normaliser, while the slice's copies are in flight.
-    const float tail = tail_in;
+    // The teacher's weights, while the slice's copies are in flight.
     float v[SSD_MAX_TOP / 32];
     float top = -INFINITY;
 #pragma unroll
@@ -353,21 +416,16 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
     }
     top = warp_max_nan(top);
     int f = 0;
-    if (!(top < INFINITY) || !(tail < INFINITY)) f = SSD_ROW_NONFINITE;  // NaN or +inf
-    if (!(top > -INFINITY) && !(tail > -INFINITY)) f = SSD_ROW_NONFINITE;  // a teacher without any mass
-    const double at_top = fmax(static_cast<double>(top) * invT, static_cast<double>(tail));
+    if (!(top < INFINITY) || !(tail_in < INFINITY)) f = SSD_ROW_NONFINITE;     // NaN or +inf
+    if (!(top > -INFINITY) && !(tail_in > -INFINITY)) f = SSD_ROW_NONFINITE;  // a teacher without any mass
+    const double at_top = fmax(static_cast<double>(top) * invT, static_cast<double>(tail_in));
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < SSD_MAX_TOP / 32; ++i)
       if (i * 32 < a.M) sum += ex2(static_cast<float>((static_cast<double>(v[i]) * invT - at_top) * 1.4426950408889634));
-    double total = warp_sum_d(static_cast<double>(sum));
-    if (lane == 0) {
-      total += static_cast<double>(ex2(static_cast<float>((static_cast<double>(tail) - at_top) * 1.4426950408889634)));
-      const double norm = at_top + log(total);
-      norm_s = norm;
-      log_p_tail_s = static_cast<double>(tail) - norm;
-      teacher_flags = f;
-    }
+    const float e_tail = ex2(static_cast<float>((static_cast<double>(tail_in) - at_top) * 1.4426950408889634));
+    sum = warp_sum(sum) + e_tail;
+    if (lane == 0) teacher = DistillTeacher{at_top, static_cast<double>(sum), 1.f / sum, e_tail / sum, f};
   }
   // Is a token there twice?  The other warps look, while the first is busy.
   for (int m = tid - 32; m >= 0 && m < a.M; m += kRowThreads - 32) {
@@ -392,13 +450,13 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
   }
   __syncthreads();
 
-  const double log_p = static_cast<double>(t) * invT - norm_s;
-  const float p = ex2(static_cast<float>(log_p * 1.4426950408889634));
+  const double t_rel = static_cast<double>(t) * invT - teacher.top;
+  const float p = ex2(static_cast<float>(t_rel * 1.4426950408889634)) * teacher.inv_total;
   {
     const float m = warp_max_nan(slice_max<TIn>(data, s.count));
     if (!(m < INFINITY)) flags |= SSD_ROW_NONFINITE;
     const float ref = is_number(m) ? m : 0.f;
-    const float sum = warp_sum(slice_exp_sum<TIn>(data, s.count, ref, c));
+    float sum = warp_sum(slice_exp_sum<TIn>(data, s.count, ref, c));
     float am = -INFINITY, as = 0.f;
     double num = 0.0, weight = 0.0;
     if (warp * 32 < a.M) {
@@ -407,110 +465,119 @@ __global__ void __launch_bounds__(kRowThreads) ssd_distill_kernel(const DistillA
       if (!is_number(am)) am = 0.f;
       as = warp_sum(ex2((z_atom - am) * c));
       weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
-      num = warp_sum_d(mine && p > 0.f ? static_cast<double>(p) * (log_p - static_cast<double>(z_atom) * invT) : 0.0);
+      num = warp_sum_d(mine && p > 0.f ? static_cast<double>(p) * (t_rel - static_cast<double>(z_atom) * invT) : 0.0);
     }
-    flags = __reduce_or_sync(0xFFFFFFFFu, flags);
-    if (lane == 0) parts[warp] = DistillPart{num, weight, ref, sum, am, as, flags | teacher_flags};
+    flags = __reduce_or_sync(0xFFFFFFFFu, flags) | teacher.flags;
+    if (flags) sum = __int_as_float(0x7FC00000);
+    if (lane == 0) warps[warp] = DistillPart{ref, sum, am, as, num, weight, flags};
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // The CTA's part, written into every CTA of the cluster (its loss terms
+    // only into the first): a few remote stores, and after the barrier every
+    // read is local.  Reading the warps' parts remotely from every warp cost
+    // more than the sums themselves.
+    DistillPart q = {};
+    if (lane < kRowWarps) q = warps[lane];
+    float tm = q.tail_sum > 0.f ? q.tail_max : -INFINITY, am = q.atom_sum > 0.f ? q.atom_max : -INFINITY;
+    tm = warp_max_nan(tm);
+    am = warp_max_nan(am);
+    const int fl = __reduce_or_sync(0xFFFFFFFFu, q.flags);
+    const float ts = warp_sum8(q.tail_sum > 0.f ? q.tail_sum * ex2((q.tail_max - tm) * c) : 0.f);
+    const float as = warp_sum8(q.atom_sum > 0.f ? q.atom_sum * ex2((q.atom_max - am) * c) : 0.f);
+    const double num = warp_sum8(q.numer), weight = warp_sum8(q.weight);
+    const DistillPart out = {tm, fl ? __int_as_float(0x7FC00000) : ts, am, as, num, weight, fl};
+    if (lane < C) {
+      DistillPart* to = cluster.map_shared_rank(&parts[0], lane) + rank;
+      *reinterpret_cast<float4*>(to) = make_float4(out.tail_max, out.tail_sum, out.atom_max, out.atom_sum);
+      if (lane == 0) {
+        to->numer = out.numer;
+        to->weight = out.weight;
+        to->flags = out.flags;
+      }
+    }
   }
   cluster.sync();
 
-  // One warp of every CTA joins the warps' parts, at most two per lane, in the
-  // same order, so all hold the same bits.
-  const double w = static_cast<double>(scale) * invT;
-  if (warp == 0) {
-    DistillPart q[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      q[i] = DistillPart{};
-      const int r = (i * 32 + lane) / kRowWarps;
-      if (r < C) q[i] = cluster.map_shared_rank(&parts[0], r)[lane % kRowWarps];
-    }
-    float tail_max = -INFINITY, atom_max = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (q[i].tail_sum > 0.f) tail_max = fmaxf(tail_max, q[i].tail_max);
-      if (q[i].atom_sum > 0.f) atom_max = fmaxf(atom_max, q[i].atom_max);
-    }
-    tail_max = warp_max_nan(tail_max);
-    atom_max = warp_max_nan(atom_max);
-    int fl = __reduce_or_sync(0xFFFFFFFFu, q[0].flags | q[1].flags);
-    double tail = 0.0, atom = 0.0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (q[i].tail_sum > 0.f)
-        tail += static_cast<double>(q[i].tail_sum) * static_cast<double>(ex2((q[i].tail_max - tail_max) * c));
-      if (q[i].atom_sum > 0.f)
-        atom += static_cast<double>(q[i].atom_sum) * static_cast<double>(ex2((q[i].atom_max - atom_max) * c));
-    }
-    tail = warp_sum_d(tail);
-    atom = warp_sum_d(atom);
-    const double num = warp_sum_d(q[0].numer + q[1].numer), weight = warp_sum_d(q[0].weight + q[1].weight);
-    // both around the larger maximum: the smaller one's factor is a true 64-bit
-    // exponential, and the tail's own logarithm is kept where it underflows
-    const double at_top = static_cast<double>(fmaxf(tail_max, atom_max));
-    const float other = tail_max > atom_max ? atom_max : tail_max;
-    const double factor = other > -INFINITY ? exp((static_cast<double>(other) - at_top) * invT) : 0.0;
-    const double total = tail_max > atom_max ? tail + atom * factor : tail * factor + atom;
-    const double logs = log(lane == 0 ? total : tail);  // two logarithms at once
-    const double lse = at_top * invT + __shfl_sync(0xFFFFFFFFu, logs, 0);
-    const double lse_tail = tail > 0.0 ? static_cast<double>(tail_max) * invT + __shfl_sync(0xFFFFFFFFu, logs, 1) : -INFINITY;
-    if (lane == 0) {
-      if (!(total > 0.0)) fl |= SSD_ROW_NONFINITE;  // every logit is -inf
-      const bool bad = (fl & SSD_ROW_INVALID) != 0;
-      const double log_p_tail = log_p_tail_s;
-      const double p_tail = static_cast<double>(ex2(static_cast<float>(log_p_tail * 1.4426950408889634)));
-      if (rank == 0) {
-        double loss = num + weight * lse;
-        if (p_tail > 0.0) loss += p_tail * (log_p_tail - lse_tail + lse);
-        if (!bad && !(loss < INFINITY)) fl |= SSD_ROW_ZERO_Q;
-        a.loss[row] = bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);
-        a.status[row] = fl;
-      }
-      const double q_tail = (tail_max > atom_max ? tail : tail * factor) / total;
-      join.lse = lse;
-      join.k = bad || !(tail > 0.0) ? 0.f : static_cast<float>(w * (q_tail - p_tail) / tail);
-      join.ref = tail > 0.0 ? tail_max : 0.f;
-      join.bad = bad;
-    }
-  }
-  __syncthreads();
-  cluster.barrier_arrive();  // this CTA has read the others' parts
+  // Every warp joins the cluster's parts for itself, in the same order, in 32
+  // bits: all the gradient needs.
+  float4 q = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  if (lane < C) q = *reinterpret_cast<const float4*>(&parts[lane]);
+  const float tail_max = warp_max_nan(q.x), atom_max = warp_max_nan(q.z);
+  const float tail = warp_sum8(q.y == 0.f ? 0.f : q.y * ex2((q.x - tail_max) * c));  // NaN stays
+  const float atom = warp_sum8(q.w == 0.f ? 0.f : q.w * ex2((q.z - atom_max) * c));
+  const float at_top = fmaxf(tail_max, atom_max);
+  const float tail_share = tail_max > -INFINITY ? tail * ex2((tail_max - at_top) * c) : 0.f;
+  const float total = tail_share + (atom_max > -INFINITY ? atom * ex2((atom_max - at_top) * c) : 0.f);
+  const bool bad = !(tail >= 0.f) || !(total > 0.f);  // a void row; every logit -inf
+
+  const float w = scale * static_cast<float>(invT);
   if (dst) {
-    const bool bad = join.bad;
-    const f32x2 k2 = f2_pack(join.k, join.k), r2 = f2_pack(-join.ref, -join.ref), c2 = f2_pack(c, c);
+    const float k = bad || !(tail > 0.f) ? 0.f : w * (tail_share / total - teacher.p_tail) / tail;
+    const float r0 = tail > 0.f ? tail_max : 0.f;
     // whole vectors only where the row's places in both tensors agree modulo 16 bytes
     const bool same = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(src)) & 15u) == 0;
+    const int shift = s.first * VE - s.head;  // the token of the slice's first place
+    const int whole0 = same ? (shift < 0 ? 1 : 0) : s.count, whole1 = same ? min(s.count, (a.V - shift) / VE) : s.count;
+    const GradOf<TIn> gradient(k, r0, c);
+    if (k == 0.f) {  // also a void row, whose logits may be NaN
 #pragma unroll 2
-    for (int i = tid; i < s.count; i += kRowThreads) {
-      f32x2 f[VE / 2];
-      float g[VE];
-      Elem<TIn>::unpack2(data[i], f);
+      for (int i = whole0 + tid; i < whole1; i += kRowThreads)
+        *reinterpret_cast<uint4*>(dst + shift + i * VE) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll 2
+      for (int i = whole0 + tid; i < whole1; i += kRowThreads)
+        *reinterpret_cast<uint4*>(dst + shift + i * VE) = gradient(data[i]);
+    }
+    // the vectors at the row's edges, or all of them
+    const auto by_element = [&](int i) {
+      const uint4 g = k == 0.f ? make_uint4(0u, 0u, 0u, 0u) : gradient(data[i]);
+      const TIn* e = reinterpret_cast<const TIn*>(&g);
 #pragma unroll
-      for (int e = 0; e < VE / 2; ++e) {
-        float x, y;
-        f2_unpack(f2_mul(f2_add(f[e], r2), c2), x, y);
-        f2_unpack(f2_mul(f2_pack(ex2(x), ex2(y)), k2), g[2 * e], g[2 * e + 1]);
+      for (int j = 0; j < VE; ++j) {
+        const int v = shift + i * VE + j;
+        if (v >= 0 && v < a.V) dst[v] = e[j];
       }
-      if (bad) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) g[e] = 0.f;
-      }
-      const int v = (s.first + i) * VE - s.head;
-      if (same && v >= 0 && v + VE <= a.V) {
-        *reinterpret_cast<uint4*>(dst + v) = Elem<TIn>::pack(g);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (v + e >= 0 && v + e < a.V) dst[v + e] = Elem<TIn>::from_float(g[e]);
-      }
+    };
+    if (same) {
+      if (tid == 0 && whole0 == 1 && s.count > 0) by_element(0);
+      if (tid == 32 && whole1 < s.count && whole1 >= whole0) by_element(whole1);
+    } else {
+      for (int i = tid; i < s.count; i += kRowThreads) by_element(i);
     }
     __syncthreads();  // the atoms' places are written after the vectors that hold them
-    if (mine && !bad) {
-      const double q = static_cast<double>(ex2(static_cast<float>((static_cast<double>(z_atom) * invT - join.lse) * 1.4426950408889634)));
-      dst[id] = Elem<TIn>::from_float(static_cast<float>(w * (q - static_cast<double>(p))));
+    if (mine && !bad) dst[id] = Elem<TIn>::from_float(w * (ex2((z_atom - at_top) * c) / total - p));
+  }
+  if (rank == 0 && warp == 0) {
+    // The loss is made of differences of logarithms: 64 bits.
+    const DistillPart* own = &parts[lane < C ? lane : 0];
+    const bool on = lane < C;
+    const double tail_d =
+        warp_sum8(on && q.y > 0.f ? static_cast<double>(q.y) * static_cast<double>(ex2((q.x - tail_max) * c)) : 0.0);
+    const double atom_d =
+        warp_sum8(on && q.w > 0.f ? static_cast<double>(q.w) * static_cast<double>(ex2((q.z - atom_max) * c)) : 0.0);
+    const double num = warp_sum8(on ? own->numer : 0.0), weight = warp_sum8(on ? own->weight : 0.0);
+    int fl = __reduce_or_sync(0xFFFFFFFFu, on ? own->flags : 0);
+    // Both around the larger maximum; the tail's own logarithm is kept where its share underflows.
+    const float other = tail_max > atom_max ? atom_max : tail_max;
+    const double factor = other > -INFINITY ? exp((static_cast<double>(other) - static_cast<double>(at_top)) * invT) : 0.0;
+    const double total_d = tail_max > atom_max ? tail_d + atom_d * factor : tail_d * factor + atom_d;
+    // three logarithms at once
+    const double logs = log(lane == 0 ? total_d : (lane == 1 ? tail_d : teacher.total));
+    const double lse = static_cast<double>(at_top) * invT + __shfl_sync(0xFFFFFFFFu, logs, 0);
+    const double lse_tail =
+        tail_d > 0.0 ? static_cast<double>(tail_max) * invT + __shfl_sync(0xFFFFFFFFu, logs, 1) : -INFINITY;
+    const double norm = __shfl_sync(0xFFFFFFFFu, logs, 2);
+    if (lane == 0) {
+      const double p_tail = static_cast<double>(teacher.p_tail);
+      double loss = num + weight * (lse - norm);
+      if (p_tail > 0.0) loss += p_tail * (static_cast<double>(tail_in) - teacher.top - norm - lse_tail + lse);
+      if (!(total_d > 0.0)) fl |= SSD_ROW_NONFINITE;
+      if (!bad && !(loss < INFINITY)) fl |= SSD_ROW_ZERO_Q;
+      a.loss[row] = bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);
+      a.status[row] = fl;
     }
   }
-  cluster.barrier_wait();  // no CTA leaves while another may read its parts
 }
 
 // ---------------------------------------------------------------------------
@@ -524,7 +591,8 @@ struct TopArgs {
   float* tail;      // [rows]
   int32_t* status;  // [rows]
   int V, M, slice_vecs;
-  float T;
+  double inv_t;   // 1 / T
+  float log2e_t;  // log2(e) / T
 };
 
 // What a CTA of a row tells the others.
@@ -596,8 +664,8 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
                    row_offset(a.in.batch_stride, a.in.row_stride, a.in.rows_per_batch, row);
   const Slice s = slice_of(src, a.V, a.slice_vecs, rank);
   const int base = s.first * VE - s.head;  // token id of the first staged place
-  const double invT = 1.0 / static_cast<double>(a.T);
-  const float c = static_cast<float>(1.4426950408889634 * invT);
+  const double invT = a.inv_t;
+  const float c = a.log2e_t;
 
   if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
   if (tid == 0) n_cand = 0;

@@ -331,7 +331,8 @@ ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_
   RowPlan p;
   if (!row_plan(rows, V, esize, kTopMinBytes, &p)) return SSD_ERR_UNSUPPORTED;
   TopArgs a;
-  a.in = RowsIn{logits, batch_stride, row_stride, rows_per_batch};
+  const bool one = n_batch == 1 || batch_stride == row_stride * rows_per_batch;
+  a.in = RowsIn{logits, batch_stride, row_stride, one ? 0 : rows_per_batch};
   a.tokens = tokens;
   a.values = values;
   a.lse = lse;
@@ -340,7 +341,8 @@ ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_
   a.V = V;
   a.M = M;
   a.slice_vecs = p.slice_vecs;
-  a.T = T;
+  a.inv_t = 1.0 / static_cast<double>(T);
+  a.log2e_t = static_cast<float>(1.4426950408889634 * a.inv_t);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == SSD_DTYPE_BF16 ? launch_rows(&ssd_top_kernel<uint16_t>, a, rows, p, s)
                                  : launch_rows(&ssd_top_kernel<float>, a, rows, p, s);
@@ -363,7 +365,10 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
   RowPlan p;
   if (!row_plan(rows, V, esize, 0, &p)) return SSD_ERR_UNSUPPORTED;
   DistillArgs a;
-  a.in = RowsIn{logits, batch_stride, row_stride, rows_per_batch};
+  // rows of one stride need no division by rows_per_batch
+  const auto flat = [&](int64_t b, int64_t r) { return n_batch == 1 || b == r * rows_per_batch; };
+  const bool one = flat(batch_stride, row_stride) && (!grad || flat(grad_batch_stride, grad_row_stride));
+  a.in = RowsIn{logits, batch_stride, row_stride, one ? 0 : rows_per_batch};
   a.tokens = tokens;
   a.values = values;
   a.tail = tail;
@@ -376,7 +381,8 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
   a.V = V;
   a.M = M;
   a.slice_vecs = p.slice_vecs;
-  a.T = T;
+  a.inv_t = 1.0 / static_cast<double>(T);
+  a.log2e_t = static_cast<float>(1.4426950408889634 * a.inv_t);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == SSD_DTYPE_BF16 ? launch_rows(&ssd_distill_kernel<uint16_t>, a, rows, p, s)
                                  : launch_rows(&ssd_distill_kernel<float>, a, rows, p, s);

@@ -318,10 +318,22 @@ def test_distill_void_rows(dtype, V):
 
 
 @pytest.mark.gpu
-def test_distill_extreme_temperatures():
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_distill_offset_logits(dtype):
+    """Logits far from zero: the exponentials' arguments are differences."""
+    V = 3000
+    z = (logits_like((3,), V, FP32, 55) + 5000.0).to(dtype)
+    tokens, values, tail = teacher((3,), V, 5, 1.0, 56, True)
+    check_distill(z, tokens, values, tail, 1.0)
+    check_distill(z - 10000, tokens, values - 70, None, 0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_distill_extreme_temperatures(dtype):
     V = 2000
     for T in (1e-4, 0.05, 30.0, 1e4):
-        z = logits_like((3,), V, FP32, 51, spread=min(2.0, 20 * T))
+        z = logits_like((3,), V, dtype, 51, spread=min(2.0, 20 * T))
         tokens, values, tail = teacher((3,), V, 5, T, 52, True)
         check_distill(z, tokens, values * min(1.0, 10 * T), None, T)
 
