@@ -18,8 +18,7 @@ namespace ssd {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxRowCluster = 8;   // the portable cluster size
-constexpr int kCandPerCta = 512;    // top candidates one CTA may contribute
-constexpr int kCandTotal = 1024;    // candidates ranked at once
+constexpr int kPool = 448;          // top candidates ranked at once
 constexpr unsigned long long kRowWaitNs = 1000000000ull;  // limit of the wait for a slice's bytes
 
 // Rows of a [n_batch, rows_per_batch, V] tensor, strides in elements.
@@ -128,8 +127,6 @@ __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s
   const int a = lo_edge ? 1 : 0;
   const int whole = max(s.count - a - (hi_edge ? 1 : 0), 0);
   if (lane == 0) {
-    mbar_init(bar, 1);
-    mbar_init_fence();
     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(whole) * 16u);
     const char* src = reinterpret_cast<const char*>(row) - s.head * static_cast<int>(sizeof(TIn)) +
                       (static_cast<long long>(s.first) + a) * 16;
@@ -150,9 +147,9 @@ __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s
 
 // Waits for the slice's bytes.  A wait that gives up waits once more (the
 // copies still target this CTA's shared memory) before the row is flagged.
-__device__ __forceinline__ int slice_wait(uint64_t* bar) {
-  if (mbar_wait_bounded(bar, 0, kRowWaitNs)) return 0;
-  (void)mbar_wait_bounded(bar, 0, kRowWaitNs);
+__device__ __forceinline__ int slice_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_wait_bounded(bar, parity, kRowWaitNs)) return 0;
+  (void)mbar_wait_bounded(bar, parity, kRowWaitNs);
   return SSD_ROW_DEVICE_TIMEOUT;
 }
 
@@ -395,7 +392,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     return;
   }
 
-  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
+  if (warp == kRowWarps - 1) {
+    if (lane == 0) {
+      mbar_init(&bar, 1);
+      mbar_init_fence();
+    }
+    slice_load(src, a.V, s, data, &bar);
+  }
   const double invT = a.inv_t;
   const float c = a.log2e_t;
   const float t = id >= 0 ? t_in : -INFINITY;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     }
     if (twice && want >= 0) flags |= SSD_ROW_BAD_TOKEN;
   }
-  flags |= slice_wait(&bar);
+  flags |= slice_wait(&bar, 0);
 
   // Take this slice's atoms out of the staged row.
   const bool mine = id >= v0 && id < v1;
@@ -595,20 +598,21 @@ struct TopArgs {
   float log2e_t;  // log2(e) / T
 };
 
-// What a CTA of a row tells the others.
+// What a CTA of a row tells the others: the sum of its exponentials outside the
+// candidates, and how many candidates it has.
 struct TopPart {
-  float sums[kRowWarps];  // of exponentials below the threshold, per warp
-  int count;              // candidates
+  double sum;
+  int count, timeout;
 };
 
-// Rank 0 gathers the candidates where its slice was staged.
-constexpr int kTopMinBytes = kCandTotal * (sizeof(unsigned long long) + sizeof(float));
+// Rank 0 orders the candidates where its slice was staged.
+constexpr int kTopMinBytes = kPool * sizeof(float);
 
-// The row's maxima over groups of threads, kMaxima of them (a lane's group
-// covers 1, 2 or 4 threads): their M-th largest is a lower bound of the row's
-// M-th largest logit, and few logits reach it.
+// The row's maxima over groups of threads, at most kMaxima of them: their M-th
+// largest is a lower bound of the row's M-th largest logit, and few logits
+// reach it.
 constexpr int kMaxima = 512;
-static_assert(kMaxima >= 2 * SSD_MAX_TOP, "more maxima than logits asked for");
+static_assert(kMaxima >= 2 * SSD_MAX_TOP && kPool > SSD_MAX_TOP, "more maxima and places than logits asked for");
 constexpr uint32_t kKeyTimeout = 0xFFFFFFFEu;  // stands for a slice that did not arrive; a NaN's key is 0xFFFFFFFF
 
 // The key of a logit from its kKeyBits high bits: the bits below them are the
@@ -621,14 +625,15 @@ __device__ __forceinline__ uint32_t full_key(uint32_t k) {
 
 // The 16 high bits of the M-th largest of a warp's keys: two bits a pass, the
 // three counts of a pass (at most kMaxima each) in one word.
-__device__ __forceinline__ uint32_t maxima_threshold(const uint32_t (&keys)[kMaxima / 32], int M) {
+template <int kPerLane>
+__device__ __forceinline__ uint32_t maxima_threshold(const uint32_t (&keys)[kPerLane], int M) {
   uint32_t prefix = 0u;
 #pragma unroll
   for (int bit = 30; bit >= 16; bit -= 2) {
     const uint32_t c1 = prefix | (1u << bit), c2 = prefix | (2u << bit), c3 = prefix | (3u << bit);
     uint32_t n = 0u;
 #pragma unroll
-    for (int i = 0; i < kMaxima / 32; ++i)
+    for (int i = 0; i < kPerLane; ++i)
       n += (keys[i] >= c1 ? 1u : 0u) + (keys[i] >= c2 ? 1u << 10 : 0u) + (keys[i] >= c3 ? 1u << 20 : 0u);
     n = __reduce_add_sync(0xFFFFFFFFu, n);
     const int n1 = n & 1023u, n2 = (n >> 10) & 1023u, n3 = n >> 20;
@@ -637,24 +642,33 @@ __device__ __forceinline__ uint32_t maxima_threshold(const uint32_t (&keys)[kMax
   return prefix;
 }
 
+template <int kPerLane>
+__device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int n, int M) {
+  const int lane = threadIdx.x & 31;
+  uint32_t keys[kPerLane], top = 0u;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    keys[i] = i * 32 + lane < n ? all[i * 32 + lane] : 0u;
+    top = max(top, keys[i]);
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  return make_uint2(maxima_threshold(keys, M), top);
+}
+
 template <typename TIn>
-__global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
-  __shared__ uint32_t maxima[kRowThreads];
-  __shared__ uint32_t all_maxima[kMaxima];
-  __shared__ unsigned long long cand[kCandPerCta];
+  __shared__ uint32_t all_maxima[kMaxima];     // written by the cluster's CTAs
+  __shared__ unsigned long long pool[kPool];   // rank 0: the cluster's candidates, written by its CTAs
+  __shared__ TopPart parts[kMaxRowCluster];    // written by the cluster's CTAs
+  __shared__ float far_max[kMaxRowCluster];    // likewise
   __shared__ double dred[kRowWarps];
-  __shared__ float fred[kRowWarps];
   __shared__ int ired[kRowWarps];
-  __shared__ int counts[4];  // per-CTA counts exchanged by the exact select
-  __shared__ double far_sum;
-  __shared__ float far_max;
-  __shared__ int n_cand, total_s;
-  __shared__ double below_s;
-  __shared__ uint32_t tau_s, row_key_s;
-  __shared__ TopPart part;
+  __shared__ int counts[3];                    // per-CTA counts exchanged by the exact select
+  __shared__ int n_pool, n_mine;               // candidates in rank 0's pool; this CTA's
+  __shared__ uint2 tau_top;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
@@ -667,132 +681,118 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
   const double invT = a.inv_t;
   const float c = a.log2e_t;
 
-  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
-  if (tid == 0) n_cand = 0;
+  if (warp == kRowWarps - 1) {
+    if (lane == 0) {
+      mbar_init(&bar, 1);
+      mbar_init_fence();
+    }
+    slice_load(src, a.V, s, data, &bar);
+  }
+  if (tid == 0) n_pool = n_mine = 0;
   __syncthreads();
-  const bool here = slice_wait(&bar) == 0;
+  const bool here = slice_wait(&bar, 0) == 0;
+  const uint32_t my_key = here ? ord_key(slice_max<TIn>(data, s.count)) : kKeyTimeout;
+  // Groups of threads small enough for twice as many maxima as logits asked
+  // for: with half of the groups at or above the threshold, 1.4 M candidates.
+  const int cluster_up = C <= 1 ? 1 : (C <= 2 ? 2 : (C <= 4 ? 4 : 8));
+  const int per = min((a.M <= kMaxima / 4 ? kMaxima / 2 : kMaxima) / cluster_up, kRowThreads);
   {
-    uint32_t k = here ? ord_key(slice_max<TIn>(data, s.count)) : kKeyTimeout;
-    if (C > 2) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
-    if (C > 4) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
-    maxima[tid] = k;
+    uint32_t k = my_key;
+    for (int o = 1; o < kRowThreads / per; o <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, o));
+    const int group = kRowThreads / per;
+    if (tid % group == 0)
+      for (int r = 0; r < C; ++r) cluster.map_shared_rank(&all_maxima[0], r)[rank * per + tid / group] = k;
   }
   cluster.sync();
 
-  // The threshold tau.
-  {
-    const int shift = C <= 2 ? 0 : (C <= 4 ? 1 : 2);  // every (1 << shift)-th entry of a CTA's maxima counts
-    const int per = kRowThreads >> shift;
-#pragma unroll
-    for (int i = 0; i < kMaxima / kRowThreads; ++i) {
-      const int k = i * kRowThreads + tid, r = k / per;
-      all_maxima[k] = r < C ? cluster.map_shared_rank(&maxima[0], r)[(k % per) << shift] : 0u;
-    }
-  }
-  __syncthreads();
+  // The threshold tau: a cut to 16 bits is the M-th maximum or below it.
   if (warp == 0) {
-    uint32_t keys[kMaxima / 32], top = 0u;
-#pragma unroll
-    for (int i = 0; i < kMaxima / 32; ++i) {
-      keys[i] = all_maxima[i * 32 + lane];
-      top = max(top, keys[i]);
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    const uint32_t t = maxima_threshold(keys, a.M);
-    if (lane == 0) {
-      tau_s = t;
-      row_key_s = top;
-    }
+    const uint2 t = a.M <= kMaxima / 4 ? threshold_and_top<kMaxima / 64>(all_maxima, per * C, a.M)
+                                       : threshold_and_top<kMaxima / 32>(all_maxima, per * C, a.M);
+    if (lane == 0) tau_top = t;
   }
   __syncthreads();
-  const uint32_t row_key = row_key_s;
-  if (row_key >= ord_key(INFINITY) || row_key <= ord_key(-INFINITY)) {  // the same in every CTA
-    if (rank == 0) {
-      for (int i = tid; i < a.M; i += kRowThreads) {
-        a.tokens[static_cast<long long>(row) * a.M + i] = -1;
-        a.values[static_cast<long long>(row) * a.M + i] = __int_as_float(0x7FC00000);
-      }
-      if (tid == 0) {
-        a.lse[row] = a.tail[row] = __int_as_float(0x7FC00000);
-        a.status[row] = row_key == kKeyTimeout ? SSD_ROW_DEVICE_TIMEOUT : SSD_ROW_NONFINITE;
-      }
+  const uint32_t row_key = tau_top.y;
+  const auto void_row = [&](int status) {
+    if (rank != 0) return;
+    for (int i = tid; i < a.M; i += kRowThreads) {
+      a.tokens[static_cast<long long>(row) * a.M + i] = -1;
+      a.values[static_cast<long long>(row) * a.M + i] = __int_as_float(0x7FC00000);
     }
-    cluster.sync();  // no CTA leaves while another may read its maxima
+    if (tid == 0) {
+      a.lse[row] = a.tail[row] = __int_as_float(0x7FC00000);
+      a.status[row] = status;
+    }
+  };
+  if (row_key >= ord_key(INFINITY) || row_key <= ord_key(-INFINITY)) {  // the same in every CTA
+    void_row(row_key == kKeyTimeout ? SSD_ROW_DEVICE_TIMEOUT : SSD_ROW_NONFINITE);
     return;
   }
   const float row_max = key_to_float(row_key);
   // With fewer maxima than M, or M of them -inf, every logit is a candidate.
-  // (A threshold cut to 16 bits is below the M-th maximum, or that itself.)
-  const uint32_t tau_key = tau_s;
-  const float tau = tau_key <= ord_key(-INFINITY) ? -INFINITY : key_to_float(full_key<TIn>(tau_key));
-  const float ref = tau > -INFINITY ? tau : 0.f;
-  float sum;
-  {
-    const f32x2 r2 = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
-    f32x2 acc = 0ull;
-    float apart = 0.f;
-#pragma unroll 2
+  const float tau = tau_top.x <= ord_key(-INFINITY) ? -INFINITY : key_to_float(full_key<TIn>(tau_top.x));
+  float ref = tau > -INFINITY ? tau : 0.f;
+
+  // A candidate goes to rank 0's pool, and out of the staged row: what is left
+  // there is the tail.
+  int* pool_at = cluster.map_shared_rank(&n_pool, 0);
+  unsigned long long* pool_to = cluster.map_shared_rank(&pool[0], 0);
+  const auto take = [&](int i, int e, float z) {
+    const int at = atomicAdd(pool_at, 1);
+    if (at < kPool) pool_to[at] = rank_key(z, base + i * VE + e);
+    reinterpret_cast<TIn*>(data + i)[e] = Elem<TIn>::neg_inf();
+  };
+  const auto real = [&](int i, int e) {  // a place of the row, not one beside its ends
+    const int id = base + i * VE + e;
+    return id >= 0 && id < a.V;
+  };
+  if (my_key >= ord_key(tau)) {
+    int n = 0;
     for (int i = tid; i < s.count; i += kRowThreads) {
       const uint4 v = data[i];
-      if (Elem<TIn>::vec_max(v) >= tau) {
-        float f[VE];
-        Elem<TIn>::unpack(v, f);
+      if (!(Elem<TIn>::vec_max(v) >= tau)) continue;
+      float f[VE];
+      Elem<TIn>::unpack(v, f);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int id = base + i * VE + e;
-          if (f[e] >= tau) {
-            if (id >= 0 && id < a.V) {
-              const int at = atomicAdd(&n_cand, 1);
-              if (at < kCandPerCta) cand[at] = rank_key(f[e], id);
-            }
-          } else {
-            apart += ex2((f[e] - ref) * c);
-          }
+      for (int e = 0; e < VE; ++e)
+        if (f[e] >= tau && real(i, e)) {
+          // Past the pool's end nothing is kept: the row is then read again.
+          if (n < kPool) take(i, e, f[e]);
+          ++n;
         }
-      } else {
-        exp_sum<TIn>(v, r2, c2, acc);
-      }
     }
-    float x, y;
-    f2_unpack(acc, x, y);
-    sum = warp_sum(x + y + apart);
+    if (n) atomicAdd(&n_mine, n);
   }
-  if (lane == 0) part.sums[warp] = sum;
-  __syncthreads();
-  if (tid == 0) part.count = n_cand;
-  cluster.sync();
-  if (warp == 0) {
+  // Every thread sums its own vectors, so it sees its own candidates gone.
+  const auto publish = [&](float part_sum, int n, int timeout) {
+    const double b = block_reduce(static_cast<double>(part_sum), dred, OpAdd());
+    if (tid < C) cluster.map_shared_rank(&parts[0], tid)[rank] = TopPart{b, n, timeout};
+    cluster.sync();
+  };
+  const float sum = slice_exp_sum<TIn>(data, s.count, ref, c);
+  __syncthreads();  // n_mine
+  publish(sum, n_mine, 0);
+  const auto joined = [&]() {
     double b = 0.0;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (i * 32 + lane) / kRowWarps;
-      if (r < C) {
-        const TopPart* q = cluster.map_shared_rank(&part, r);
-        b += static_cast<double>(q->sums[lane % kRowWarps]);
-        if (lane % kRowWarps == 0) n += q->count > kCandPerCta ? kCandTotal + 1 : q->count;
-      }
-    }
-    b = warp_sum_d(b);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) {
-      below_s = b;
-      total_s = n;
-    }
-  }
-  __syncthreads();
-  double below = below_s;
-  int total = total_s;
-  const bool over = total > kCandTotal;
-  float ref_f = ref;
-  float limit = tau;  // the tail's logits are below it (or equal to it and counted apart)
+    for (int r = 0; r < C; ++r) b += parts[r].sum;
+    return b;
+  };
+  double below = joined();
+  int total = 0;
+  for (int r = 0; r < C; ++r) total = min(total + parts[r].count, kPool + 1);
 
-  if (over) {
-    // Exact select, for rows with many equal logits at the threshold: the
-    // M-th largest key by two bits a pass over the staged row, then the equal
-    // ones in token order.
+  if (total > kPool) {
+    // Exact select, for rows with many equal logits at the threshold: stage the
+    // row again, find the M-th largest key by two bits a pass, then take the
+    // larger ones, and the equal ones in token order.
+    __syncthreads();
+    if (warp == kRowWarps - 1) {
+      fence_proxy_async_shared();
+      slice_load(src, a.V, s, data, &bar);
+    }
+    __syncthreads();
+    const int timeout = slice_wait(&bar, 1);
     uint32_t prefix = 0u;
-    int above = 0;  // elements with a larger key than the prefix's final value
     for (int bit = 30; bit >= 32 - Elem<TIn>::kKeyBits; bit -= 2) {
       const uint32_t c1 = prefix | (1u << bit), c2 = prefix | (2u << bit), c3 = prefix | (3u << bit);
       int n1 = 0, n2 = 0, n3 = 0;
@@ -801,8 +801,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
         Elem<TIn>::unpack(data[i], f);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const int id = base + i * VE + e;
-          const uint32_t k = id >= 0 && id < a.V ? ord_key(f[e]) : 0u;
+          const uint32_t k = real(i, e) ? ord_key(f[e]) : 0u;
           n1 += k >= c1;
           n2 += k >= c2;
           n3 += k >= c3;
@@ -821,51 +820,29 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
       cluster.sync();  // read before the next pass overwrites them
       prefix = n3 >= a.M ? c3 : (n2 >= a.M ? c2 : (n1 >= a.M ? c1 : prefix));
     }
-    int gt = 0, eq = 0;
     const float kth = key_to_float(full_key<TIn>(prefix));
-    const float kref = kth > -INFINITY ? kth : 0.f;
-    if (tid == 0) n_cand = 0;
-    __syncthreads();
-    sum = 0.f;
+    if (tid == 0) n_pool = 0;
+    int gt = 0, eq = 0;
     for (int i = tid; i < s.count; i += kRowThreads) {
       float f[VE];
       Elem<TIn>::unpack(data[i], f);
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const int id = base + i * VE + e;
-        if (id < 0 || id >= a.V) continue;
-        if (f[e] > kth) {
-          ++gt;
-          const int at = atomicAdd(&n_cand, 1);
-          if (at < kCandPerCta) cand[at] = rank_key(f[e], id);  // fewer than M <= kCandPerCta in all
-        } else if (f[e] == kth) {
-          ++eq;
-        } else {
-          sum += ex2((f[e] - kref) * c);
-        }
+        gt += real(i, e) && f[e] > kth;
+        eq += real(i, e) && f[e] == kth;
       }
     }
-    below = block_reduce(static_cast<double>(sum), dred, OpAdd());
     gt = block_reduce(gt, ired, OpAdd());
     eq = block_reduce(eq, ired, OpAdd());
-    if (tid == 0) {
-      counts[0] = gt, counts[1] = eq;
-      far_sum = below;
-    }
+    if (tid == 0) counts[0] = gt, counts[1] = eq;
     cluster.sync();
-    int eq_before = 0, eq_all = 0;
-    below = 0.0;
+    int need = a.M, taken = 0;  // of the equal ones, in token order; those in earlier slices
     for (int r = 0; r < C; ++r) {
       const int* q = cluster.map_shared_rank(&counts[0], r);
-      above += q[0];
-      if (r < rank) eq_before += q[1];
-      eq_all += q[1];
-      below += *cluster.map_shared_rank(&far_sum, r);
+      need -= q[0];
+      if (r < rank) taken += q[1];
     }
-    const int need = a.M - above;  // of the equal ones, in token order
-    int taken = eq_before;
-    __syncthreads();
-    for (int i0 = 0; i0 < s.count && taken < need; i0 += kRowThreads) {  // uniform over the CTA
+    for (int i0 = 0; i0 < s.count; i0 += kRowThreads) {
       const int i = i0 + tid;
       float f[VE];
       int n = 0;
@@ -873,8 +850,8 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
         Elem<TIn>::unpack(data[i], f);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const int id = base + i * VE + e;
-          n += id >= 0 && id < a.V && f[e] == kth;
+          if (!real(i, e)) f[e] = __int_as_float(0x7FC00000);  // equal to nothing
+          n += f[e] == kth;
         }
       }
       int inc = n;
@@ -884,92 +861,62 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
         if (lane >= o) inc += y;
       }
       __syncthreads();
-      if (lane == 31) ired[tid >> 5] = inc;
+      if (lane == 31) ired[warp] = inc;
       __syncthreads();
       int before = taken + inc - n, chunk = 0;
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) {
-        if (w < (tid >> 5)) before += ired[w];
+        if (w < warp) before += ired[w];
         chunk += ired[w];
       }
-      if (n > 0) {
+      if (i < s.count) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const int id = base + i * VE + e;
-          if (id >= 0 && id < a.V && f[e] == kth) {
-            if (before < need) {
-              const int at = atomicAdd(&n_cand, 1);
-              if (at < kCandPerCta) cand[at] = rank_key(kth, id);
-            }
+          if (f[e] > kth) take(i, e, f[e]);
+          if (f[e] == kth) {
+            if (before < need) take(i, e, f[e]);
             ++before;
           }
         }
       }
       taken += chunk;
     }
-    __syncthreads();
-    if (tid == 0) part.count = n_cand;
-    ref_f = kref;
-    limit = kth;
-    if (kth > -INFINITY) below += static_cast<double>(eq_all - need);
-    cluster.sync();
+    ref = kth > -INFINITY ? kth : 0.f;
+    publish(slice_exp_sum<TIn>(data, s.count, ref, c), 0, timeout);
+    below = joined();
     total = a.M;
+    int late = 0;
+    for (int r = 0; r < C; ++r) late |= parts[r].timeout;
+    if (late) {
+      void_row(SSD_ROW_DEVICE_TIMEOUT);
+      return;
+    }
   }
 
   // A tail far below the threshold: sum it again around its own maximum.
   if (total == a.M && a.V > a.M && below < 1e-18) {
+    const float m = warp_max_nan(slice_max<TIn>(data, s.count));
+    const double tm_cta = block_reduce(static_cast<double>(m), dred, OpMax());
+    if (tid < C) cluster.map_shared_rank(&far_max[0], tid)[rank] = static_cast<float>(tm_cta);
+    cluster.sync();
     float tm = -INFINITY;
-    for (int i = tid; i < s.count; i += kRowThreads) {
-      float f[VE];
-      Elem<TIn>::unpack(data[i], f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (f[e] < limit) tm = fmaxf(tm, f[e]);
-    }
-    tm = block_reduce(tm, fred, OpMax());
-    if (tid == 0) far_max = tm;
-    cluster.sync();
-    tm = -INFINITY;
-    for (int r = 0; r < C; ++r) tm = fmaxf(tm, *cluster.map_shared_rank(&far_max, r));
-    sum = 0.f;
-    if (tm > -INFINITY)
-      for (int i = tid; i < s.count; i += kRowThreads) {
-        float f[VE];
-        Elem<TIn>::unpack(data[i], f);
-#pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (f[e] < limit) sum += ex2((f[e] - tm) * c);
-      }
-    below = block_reduce(static_cast<double>(sum), dred, OpAdd());
-    if (tid == 0) far_sum = below;
-    cluster.sync();
-    below = 0.0;
-    for (int r = 0; r < C; ++r) below += *cluster.map_shared_rank(&far_sum, r);
-    if (tm > -INFINITY) ref_f = tm;
+    for (int r = 0; r < C; ++r) tm = fmaxf(tm, far_max[r]);
+    if (tm > -INFINITY) ref = tm;
+    publish(slice_exp_sum<TIn>(data, s.count, ref, c), 0, 0);
+    below = joined();
   }
+  if (rank != 0) return;  // every write into another CTA is behind a cluster barrier
 
-  if (rank != 0) {
-    cluster.sync();  // rank 0 has read this CTA's candidates
-    return;
-  }
-  // Gather and rank the candidates; those past the M-th belong to the tail.
-  // The sums run over the ranked order, whatever order the candidates came in.
-  unsigned long long* pool = reinterpret_cast<unsigned long long*>(data);
-  float* ranked = reinterpret_cast<float*>(pool + kCandTotal);
+  // Order the candidates; those past the M-th belong to the tail. The sums run
+  // over the order, whatever order the candidates came in.
+  float* ranked = reinterpret_cast<float*>(data);
+  const int n = min(n_pool, kPool);
   __syncthreads();  // the staged logits are no longer read
-  int off = 0;
-  for (int r = 0; r < C; ++r) {
-    const int n = min(cluster.map_shared_rank(&part, r)->count, kCandPerCta);
-    const unsigned long long* q = cluster.map_shared_rank(&cand[0], r);
-    for (int i = tid; i < n && off + i < kCandTotal; i += kRowThreads) pool[off + i] = q[i];
-    off = min(off + n, kCandTotal);
-  }
-  cluster.sync();
-  for (int i = tid; i < off; i += kRowThreads) {
+  for (int i = tid; i < n; i += kRowThreads) {
     const unsigned long long k = pool[i];
     int pos = 0;
 #pragma unroll 4
-    for (int j = 0; j < off; ++j) pos += pool[j] > k;
+    for (int j = 0; j < n; ++j) pos += pool[j] > k;
     const float z = key_to_float(static_cast<uint32_t>(k >> 32));
     ranked[pos] = z;
     if (pos < a.M) {
@@ -979,22 +926,24 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_kernel(const TopArgs a) {
     }
   }
   __syncthreads();
+  // where every logit was a candidate, the tail's largest is the reference
+  if (!(below > 0.0) && n > a.M) ref = ranked[a.M] > -INFINITY ? ranked[a.M] : 0.f;
   float top_sum = 0.f, rest = 0.f;
-  for (int i = tid; i < off; i += kRowThreads) {
+  for (int i = tid; i < n; i += kRowThreads) {
     const float z = ranked[i];
     if (i < a.M)
       top_sum += ex2((z - row_max) * c);
     else
-      rest += ex2((z - ref_f) * c);
+      rest += ex2((z - ref) * c);
   }
   const double top_d = block_reduce(static_cast<double>(top_sum), dred, OpAdd());
   const double rest_d = block_reduce(static_cast<double>(rest), dred, OpAdd());
   if (warp == 0) {
-    const double t = below + rest_d;  // around ref_f
-    const double share = t > 0.0 ? t * exp((static_cast<double>(ref_f) - static_cast<double>(row_max)) * invT) : 0.0;
+    const double t = below + rest_d;  // around ref
+    const double share = t > 0.0 ? t * exp((static_cast<double>(ref) - static_cast<double>(row_max)) * invT) : 0.0;
     const double logs = log(lane == 0 ? t : top_d + share);  // two logarithms at once
     if (lane == 0) {
-      a.tail[row] = t > 0.0 ? static_cast<float>(static_cast<double>(ref_f) * invT + logs) : -INFINITY;
+      a.tail[row] = t > 0.0 ? static_cast<float>(static_cast<double>(ref) * invT + logs) : -INFINITY;
       a.status[row] = 0;
     }
     if (lane == 1) a.lse[row] = static_cast<float>(static_cast<double>(row_max) * invT + logs);
