@@ -410,22 +410,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
 
   if (warp == 0) {
     // The teacher's weights, while the slice's copies are in flight.
-    float v[SSD_MAX_TOP / 32];
     float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < SSD_MAX_TOP / 32; ++i) {
-      v[i] = i * 32 < a.M ? atoms[i * 32 + lane] : -INFINITY;
-      top = fmax_nan(top, v[i]);
-    }
+#pragma unroll 1
+    for (int i = lane; i < a.M; i += 32) top = fmax_nan(top, atoms[i]);
     top = warp_max_nan(top);
     int f = 0;
     if (!(top < INFINITY) || !(tail_in < INFINITY)) f = SSD_ROW_NONFINITE;     // NaN or +inf
     if (!(top > -INFINITY) && !(tail_in > -INFINITY)) f = SSD_ROW_NONFINITE;  // a teacher without any mass
     const double at_top = fmax(static_cast<double>(top) * invT, static_cast<double>(tail_in));
     float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < SSD_MAX_TOP / 32; ++i)
-      if (i * 32 < a.M) sum += ex2(static_cast<float>((static_cast<double>(v[i]) * invT - at_top) * 1.4426950408889634));
+#pragma unroll 1
+    for (int i = lane; i < a.M; i += 32)
+      sum += ex2(static_cast<float>((static_cast<double>(atoms[i]) * invT - at_top) * 1.4426950408889634));
     const float e_tail = ex2(static_cast<float>((static_cast<double>(tail_in) - at_top) * 1.4426950408889634));
     sum = warp_sum(sum) + e_tail;
     if (lane == 0) teacher = DistillTeacher{at_top, static_cast<double>(sum), 1.f / sum, e_tail / sum, f};
@@ -598,6 +594,29 @@ struct TopArgs {
   float log2e_t;  // log2(e) / T
 };
 
+// A thread's two largest vectors by their largest element, and where the first
+// of them is: few threads need to look at more than that one for candidates.
+struct TwoMax {
+  float first, second;  // NaN in the second when any element is
+  int at;
+};
+template <typename TIn>
+__device__ __forceinline__ TwoMax slice_two_max(const uint4* data, int count) {
+  TwoMax m = {-INFINITY, -INFINITY, static_cast<int>(threadIdx.x)};
+#pragma unroll 2
+  for (int i = threadIdx.x; i < count; i += kRowThreads) {
+    const float v = Elem<TIn>::vec_max(data[i]);
+    if (v > m.first) {
+      m.second = fmax_nan(m.second, m.first);
+      m.first = v;
+      m.at = i;
+    } else {
+      m.second = fmax_nan(m.second, v);
+    }
+  }
+  return m;
+}
+
 // What a CTA of a row tells the others: the sum of its exponentials outside the
 // candidates, and how many candidates it has.
 struct TopPart {
@@ -623,36 +642,50 @@ __device__ __forceinline__ uint32_t full_key(uint32_t k) {
   return k;
 }
 
-// The 16 high bits of the M-th largest of a warp's keys: two bits a pass, the
-// three counts of a pass (at most kMaxima each) in one word.
-template <int kPerLane>
-__device__ __forceinline__ uint32_t maxima_threshold(const uint32_t (&keys)[kPerLane], int M) {
-  uint32_t prefix = 0u;
-#pragma unroll
-  for (int bit = 30; bit >= 16; bit -= 2) {
-    const uint32_t c1 = prefix | (1u << bit), c2 = prefix | (2u << bit), c3 = prefix | (3u << bit);
-    uint32_t n = 0u;
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i)
-      n += (keys[i] >= c1 ? 1u : 0u) + (keys[i] >= c2 ? 1u << 10 : 0u) + (keys[i] >= c3 ? 1u << 20 : 0u);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    const int n1 = n & 1023u, n2 = (n >> 10) & 1023u, n3 = n >> 20;
-    prefix = n3 >= M ? c3 : (n2 >= M ? c2 : (n1 >= M ? c1 : prefix));
-  }
-  return prefix;
-}
-
+// A threshold that at least M of a warp's keys reach, and no more than about
+// M / 4 above that, by quartering the range of the keys' 16 high bits; and the
+// largest key.  One warp runs through it while the others wait, so it is a loop
+// of few instructions: a search of all 16 bits took 3600 cycles, and 5900
+// unrolled, since straight-line code waits for its instructions.
 template <int kPerLane>
 __device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int n, int M) {
   const int lane = threadIdx.x & 31;
-  uint32_t keys[kPerLane], top = 0u;
+  uint32_t keys[kPerLane], top = 0u, low = 0xFFFFFFFFu;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     keys[i] = i * 32 + lane < n ? all[i * 32 + lane] : 0u;
     top = max(top, keys[i]);
+    low = min(low, keys[i]);
+    keys[i] >>= 16;
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  return make_uint2(maxima_threshold(keys, M), top);
+  low = __reduce_min_sync(0xFFFFFFFFu, low) >> 16;
+  uint32_t high = (top >> 16) + 1u;  // fewer than M reach `high`, at least M reach `low`
+  if (n < M) low = 0u;
+#pragma unroll 1
+  while (high - low > 1u && n >= M) {
+    const uint32_t d = high - low, m1 = low + (d + 3) / 4, m2 = low + (d + 1) / 2, m3 = low + (3 * d + 3) / 4;
+    uint32_t k = 0u;  // three counts of at most kMaxima
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      k += (keys[i] >= m1 ? 1u : 0u) + (keys[i] >= m2 ? 1u << 10 : 0u) + (keys[i] >= m3 ? 1u << 20 : 0u);
+    k = __reduce_add_sync(0xFFFFFFFFu, k);
+    const int n1 = k & 1023u, n2 = (k >> 10) & 1023u, n3 = k >> 20;
+    const int reach = n3 >= M ? n3 : (n2 >= M ? n2 : n1);
+    if (n3 >= M) {
+      low = m3;
+    } else if (n2 >= M) {
+      low = m2;
+      high = min(high, m3);
+    } else if (n1 >= M) {
+      low = m1;
+      high = min(high, m2);
+    } else {
+      high = min(high, m1);
+    }
+    if (reach >= M && reach <= M + M / 4 + 4) break;
+  }
+  return make_uint2(low << 16, top);
 }
 
 template <typename TIn>
@@ -661,13 +694,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
   __shared__ uint32_t all_maxima[kMaxima];     // written by the cluster's CTAs
-  __shared__ unsigned long long pool[kPool];   // rank 0: the cluster's candidates, written by its CTAs
+  __shared__ unsigned long long pool[kPool];   // the CTA's candidates; rank 0: then the cluster's
   __shared__ TopPart parts[kMaxRowCluster];    // written by the cluster's CTAs
   __shared__ float far_max[kMaxRowCluster];    // likewise
   __shared__ double dred[kRowWarps];
   __shared__ int ired[kRowWarps];
   __shared__ int counts[3];                    // per-CTA counts exchanged by the exact select
-  __shared__ int n_pool, n_mine;               // candidates in rank 0's pool; this CTA's
+  __shared__ int n_mine;                       // this CTA's candidates
   __shared__ uint2 tau_top;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -688,10 +721,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
     }
     slice_load(src, a.V, s, data, &bar);
   }
-  if (tid == 0) n_pool = n_mine = 0;
+  if (tid == 0) n_mine = 0;
   __syncthreads();
   const bool here = slice_wait(&bar, 0) == 0;
-  const uint32_t my_key = here ? ord_key(slice_max<TIn>(data, s.count)) : kKeyTimeout;
+  const TwoMax mine = slice_two_max<TIn>(data, s.count);
+  const uint32_t my_key = here ? ord_key(fmax_nan(mine.first, mine.second)) : kKeyTimeout;
   // Groups of threads small enough for twice as many maxima as logits asked
   // for: with half of the groups at or above the threshold, 1.4 M candidates.
   const int cluster_up = C <= 1 ? 1 : (C <= 2 ? 2 : (C <= 4 ? 4 : 8));
@@ -733,35 +767,32 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
   const float tau = tau_top.x <= ord_key(-INFINITY) ? -INFINITY : key_to_float(full_key<TIn>(tau_top.x));
   float ref = tau > -INFINITY ? tau : 0.f;
 
-  // A candidate goes to rank 0's pool, and out of the staged row: what is left
-  // there is the tail.
-  int* pool_at = cluster.map_shared_rank(&n_pool, 0);
-  unsigned long long* pool_to = cluster.map_shared_rank(&pool[0], 0);
+  // A candidate goes to the CTA's pool, and out of the staged row: what is left
+  // there is the tail.  Past the pool's end nothing is kept, and the row is read
+  // again.
   const auto take = [&](int i, int e, float z) {
-    const int at = atomicAdd(pool_at, 1);
-    if (at < kPool) pool_to[at] = rank_key(z, base + i * VE + e);
+    const int at = atomicAdd(&n_mine, 1);
+    if (at < kPool) pool[at] = rank_key(z, base + i * VE + e);
     reinterpret_cast<TIn*>(data + i)[e] = Elem<TIn>::neg_inf();
   };
   const auto real = [&](int i, int e) {  // a place of the row, not one beside its ends
     const int id = base + i * VE + e;
     return id >= 0 && id < a.V;
   };
-  if (my_key >= ord_key(tau)) {
-    int n = 0;
-    for (int i = tid; i < s.count; i += kRowThreads) {
-      const uint4 v = data[i];
-      if (!(Elem<TIn>::vec_max(v) >= tau)) continue;
-      float f[VE];
-      Elem<TIn>::unpack(v, f);
-#pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (f[e] >= tau && real(i, e)) {
-          // Past the pool's end nothing is kept: the row is then read again.
-          if (n < kPool) take(i, e, f[e]);
-          ++n;
-        }
+  const auto look = [&](int i) {
+#pragma unroll 1
+    for (int e = 0; e < VE; ++e) {
+      const float z = Elem<TIn>::to_float(reinterpret_cast<const TIn*>(data + i)[e]);
+      if (z >= tau && real(i, e)) take(i, e, z);
     }
-    if (n) atomicAdd(&n_mine, n);
+  };
+  if (s.count > tid) {
+    if (mine.second >= tau) {
+      for (int i = tid; i < s.count; i += kRowThreads)
+        if (Elem<TIn>::vec_max(data[i]) >= tau) look(i);
+    } else if (mine.first >= tau) {
+      look(mine.at);
+    }
   }
   // Every thread sums its own vectors, so it sees its own candidates gone.
   const auto publish = [&](float part_sum, int n, int timeout) {
@@ -790,6 +821,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       fence_proxy_async_shared();
       slice_load(src, a.V, s, data, &bar);
     }
+    if (tid == 0) n_mine = 0;
     __syncthreads();
     const int timeout = slice_wait(&bar, 1);
     uint32_t prefix = 0u;
@@ -821,7 +853,6 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       prefix = n3 >= a.M ? c3 : (n2 >= a.M ? c2 : (n1 >= a.M ? c1 : prefix));
     }
     const float kth = key_to_float(full_key<TIn>(prefix));
-    if (tid == 0) n_pool = 0;
     int gt = 0, eq = 0;
     for (int i = tid; i < s.count; i += kRowThreads) {
       float f[VE];
@@ -882,7 +913,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       taken += chunk;
     }
     ref = kth > -INFINITY ? kth : 0.f;
-    publish(slice_exp_sum<TIn>(data, s.count, ref, c), 0, timeout);
+    const float rest = slice_exp_sum<TIn>(data, s.count, ref, c);
+    __syncthreads();  // n_mine
+    publish(rest, n_mine, timeout);
     below = joined();
     total = a.M;
     int late = 0;
@@ -902,16 +935,25 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
     float tm = -INFINITY;
     for (int r = 0; r < C; ++r) tm = fmaxf(tm, far_max[r]);
     if (tm > -INFINITY) ref = tm;
-    publish(slice_exp_sum<TIn>(data, s.count, ref, c), 0, 0);
+    publish(slice_exp_sum<TIn>(data, s.count, ref, c), n_mine, 0);
     below = joined();
   }
-  if (rank != 0) return;  // every write into another CTA is behind a cluster barrier
+  if (rank != 0) {
+    int off = 0;
+    for (int r = 0; r < rank; ++r) off += parts[r].count;
+    unsigned long long* to = cluster.map_shared_rank(&pool[0], 0);
+    for (int i = tid; i < n_mine && off + i < kPool; i += kRowThreads) to[off + i] = pool[i];
+    cluster.barrier_arrive();  // nothing is written into this CTA any more: it need not wait
+    return;
+  }
 
   // Order the candidates; those past the M-th belong to the tail. The sums run
   // over the order, whatever order the candidates came in.
   float* ranked = reinterpret_cast<float*>(data);
-  const int n = min(n_pool, kPool);
-  __syncthreads();  // the staged logits are no longer read
+  int n = 0;
+  for (int r = 0; r < C; ++r) n += parts[r].count;
+  n = min(n, kPool);
+  cluster.sync();  // the others' candidates; the staged logits are no longer read
   for (int i = tid; i < n; i += kRowThreads) {
     const unsigned long long k = pool[i];
     int pos = 0;
