@@ -541,35 +541,40 @@ def _rows_of(t: torch.Tensor, name: str):
     or [B, R, V] view whose last dimension is dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() not in (1, 2, 3):
-        raise ValueError(f"{name} must have one to three dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n not in (1, 2, 3):
+        raise ValueError(f"{name} must have one to three dimensions, got {n}")
+    if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
-    lead, strides = (1, 1) + tuple(t.shape[:-1]), (0, 0) + tuple(t.stride()[:-1])
-    return lead[-2], lead[-1], t.shape[-1], strides[-2], strides[-1]
+    if n == 3:
+        return shape[0], shape[1], shape[2], stride[0], stride[1]
+    if n == 2:
+        return 1, shape[0], shape[1], 0, stride[0]
+    return 1, 1, shape[0], 0, 0
 
 
-_here = contextlib.nullcontext()
+def _want(t, name: str, dtype, shape, index: int):
+    """_need with the device as its index: the checks of a small call count."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, torch.device("cuda", index))
 
 
-class _Scope:
-    """The tensors' device as the current one, and `stream`, when one is given,
-    as the stream that the call's own allocations belong to."""
+# The current stream's handle without a Stream object around it (4 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
 
-    def __init__(self, device, stream):
-        self.device = _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream = _here if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        self.device.__enter__()
-        self.stream.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *e):
-        self.stream.__exit__(*e)
-        self.device.__exit__(*e)
+def _launch(index: int, stream, call):
+    """call(raw stream) with device `index` current, and `stream`, when one is
+    given, as the stream that the call's own allocations belong to."""
+    if stream is None and torch.cuda.current_device() == index:
+        return call(_raw_stream(index))
+    with torch.cuda.device(index), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
+        return call(_raw_stream(index))
 
 
 @dataclass
@@ -586,17 +591,22 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -
     e.g. target[:, :K]) with the log-mass of all and of the other tokens (see
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
-    dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
-    with _Scope(dev, stream) as st:
-        M = int(M)
-        f32 = dict(dtype=torch.float32, device=dev)
-        r = TeacherTop(tokens=torch.empty(lead + (max(M, 0),), dtype=torch.int32, device=dev),
-                       values=torch.empty(lead + (max(M, 0),), **f32), lse=torch.empty(lead, **f32),
-                       tail=torch.empty(lead, **f32), status=torch.empty(lead, dtype=torch.int32, device=dev))
-        _check(load().ssd_teacher_top(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(r.tokens),
-                                      _ptr(r.values), _ptr(r.lse), _ptr(r.tail), _ptr(r.status), st),
-               "ssd_teacher_top")
-    return r
+    dt, dev, lead = _logit_dtype(logits), logits.device, logits.shape[:-1]
+    M = int(M)
+    wide = lead + (max(M, 0),)
+
+    def call(st):
+        r = TeacherTop(tokens=torch.empty(wide, dtype=torch.int32, device=dev),
+                       values=torch.empty(wide, dtype=torch.float32, device=dev),
+                       lse=torch.empty(lead, dtype=torch.float32, device=dev),
+                       tail=torch.empty(lead, dtype=torch.float32, device=dev),
+                       status=torch.empty(lead, dtype=torch.int32, device=dev))
+        _check(load().ssd_teacher_top(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, r.tokens.data_ptr(),
+                                      r.values.data_ptr(), r.lse.data_ptr(), r.tail.data_ptr(), r.status.data_ptr(),
+                                      st), "ssd_teacher_top")
+        return r
+
+    return _launch(dev.index, stream, call)
 
 
 @dataclass
@@ -614,29 +624,37 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
     ssd_distill in ssd.h).  `grad` may be given (of the logits' shape and dtype,
     dense in its last dimension; the logits themselves are allowed)."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
-    dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
+    dt, dev, lead = _logit_dtype(logits), logits.device, logits.shape[:-1]
+    index = dev.index
     M = tokens.shape[-1] if tokens.dim() else 0
-    _need(tokens, "tokens", torch.int32, lead + (M,), dev)
-    _need(values, "values", torch.float32, lead + (M,), dev)
+    wide = lead + (M,)
+    _want(tokens, "tokens", torch.int32, wide, index)
+    _want(values, "values", torch.float32, wide, index)
     if tail is not None:
-        _need(tail, "tail", torch.float32, lead, dev)
+        _want(tail, "tail", torch.float32, lead, index)
     if row_scale is not None:
-        _need(row_scale, "row_scale", torch.float32, lead, dev)
+        _want(row_scale, "row_scale", torch.float32, lead, index)
     if grad is not None:
         if not with_grad:
             raise ValueError("grad is given but with_grad is False")
         if grad.dtype != logits.dtype or grad.device != dev or grad.shape != logits.shape:
             raise ValueError("grad must have the logits' shape, dtype and device")
-    with _Scope(dev, stream) as st:
-        if with_grad and grad is None:
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        gbs, grs = _rows_of(grad, "grad")[3:] if with_grad else (0, 0)
+
+    def call(st):
+        g = grad
+        if with_grad and g is None:
+            g = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            gbs, grs = rpb * V, V
+        else:
+            gbs, grs = _rows_of(g, "grad")[3:] if with_grad else (0, 0)
         r = DistillResult(loss=torch.empty(lead, dtype=torch.float32, device=dev),
-                          status=torch.empty(lead, dtype=torch.int32, device=dev), grad=grad)
-        _check(load().ssd_distill(_ptr(logits), dt, nb, rpb, V, bs, rs, float(T), M, _ptr(tokens), _ptr(values),
-                                  _ptr(tail), _ptr(row_scale), _ptr(r.loss), _ptr(r.status), _ptr(grad), gbs, grs,
-                                  st), "ssd_distill")
-    return r
+                          status=torch.empty(lead, dtype=torch.int32, device=dev), grad=g)
+        _check(load().ssd_distill(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, tokens.data_ptr(),
+                                  values.data_ptr(), _ptr(tail), _ptr(row_scale), r.loss.data_ptr(),
+                                  r.status.data_ptr(), _ptr(g), gbs, grs, st), "ssd_distill")
+        return r
+
+    return _launch(index, stream, call)
 
 
 def linear_ce_workspace_bytes(N: int, D: int, V: int, grad: bool) -> int:
@@ -648,14 +666,15 @@ def _linear_args(hidden, weight, targets):
     dev = hidden.device
     if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
         raise ValueError("hidden and weight must be torch.bfloat16")
-    if weight.device != dev:
+    if weight.get_device() != dev.index:
         raise ValueError(f"weight must be on {dev}, got {weight.device}")
     if weight.dim() != 2 or weight.shape[1] != D or weight.stride(1) != 1:
         raise ValueError(f"weight must be [V, {D}] and dense in its last dimension")
-    _need(targets, "targets", torch.int32, tuple(hidden.shape[:-1]), dev)
+    lead = hidden.shape[:-1]
+    _want(targets, "targets", torch.int32, lead, dev.index)
     V = weight.shape[0]
-    return dev, nb * rpb, V, (_ptr(hidden), _ptr(weight), DTYPE_BF16, nb, rpb, D, V, bs, rs,
-                              weight.stride(0) if V > 1 else max(weight.stride(0), D), _ptr(targets))
+    return dev, lead, nb * rpb, D, V, (hidden.data_ptr(), weight.data_ptr(), DTYPE_BF16, nb, rpb, D, V, bs, rs,
+                                       weight.stride(0) if V > 1 else max(weight.stride(0), D), targets.data_ptr())
 
 
 def _linear_workspace(workspace, N, D, V, grad, dev):
@@ -680,15 +699,18 @@ def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     """Cross entropy of the rows of hidden @ weight.T against `targets`
     (negative: left out), without storing the logits (see ssd_linear_ce in
     ssd.h).  hidden [..., D] (up to three dimensions) and weight [V, D] bf16."""
-    dev, N, V, args = _linear_args(hidden, weight, targets)
-    with _Scope(dev, stream) as st:
-        ws = _linear_workspace(workspace, N, hidden.shape[-1], V, False, dev)
-        f32 = dict(dtype=torch.float32, device=dev)
-        r = LinearCeResult(loss=torch.empty(targets.shape, **f32), lse=torch.empty(targets.shape, **f32),
-                           status=torch.empty(targets.shape, dtype=torch.int32, device=dev))
-        _check(load().ssd_linear_ce(*args, _ptr(r.loss), _ptr(r.lse), _ptr(r.status), _ptr(ws), ws.numel(),
-                                    st), "ssd_linear_ce")
-    return r
+    dev, lead, N, D, V, args = _linear_args(hidden, weight, targets)
+
+    def call(st):
+        ws = _linear_workspace(workspace, N, D, V, False, dev)
+        r = LinearCeResult(loss=torch.empty(lead, dtype=torch.float32, device=dev),
+                           lse=torch.empty(lead, dtype=torch.float32, device=dev),
+                           status=torch.empty(lead, dtype=torch.int32, device=dev))
+        _check(load().ssd_linear_ce(*args, r.loss.data_ptr(), r.lse.data_ptr(), r.status.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), st), "ssd_linear_ce")
+        return r
+
+    return _launch(dev.index, stream, call)
 
 
 def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
@@ -697,21 +719,27 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
                        workspace: Optional[torch.Tensor] = None, stream=None):
     """(grad_hidden, grad_weight) of sum(row_scale * loss), loss and lse being
     ssd_linear_ce's (see ssd_linear_ce_grad in ssd.h)."""
-    dev, N, V, args = _linear_args(hidden, weight, targets)
-    D = hidden.shape[-1]
-    _need(lse, "lse", torch.float32, tuple(targets.shape), dev)
+    dev, lead, N, D, V, args = _linear_args(hidden, weight, targets)
+    index = dev.index
+    _want(lse, "lse", torch.float32, lead, index)
     if row_scale is not None:
-        _need(row_scale, "row_scale", torch.float32, tuple(targets.shape), dev)
+        _want(row_scale, "row_scale", torch.float32, lead, index)
     if status is not None:
-        _need(status, "status", torch.int32, tuple(targets.shape), dev)
-    with _Scope(dev, stream) as st:
+        _want(status, "status", torch.int32, lead, index)
+    if grad_hidden is not None:
+        _want(grad_hidden, "grad_hidden", torch.bfloat16, hidden.shape, index)
+    if grad_weight is not None:
+        _want(grad_weight, "grad_weight", torch.bfloat16, (V, D), index)
+
+    def call(st):
         ws = _linear_workspace(workspace, N, D, V, True, dev)
-        if grad_hidden is None:
-            grad_hidden = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
-        if grad_weight is None:
-            grad_weight = torch.empty((V, D), dtype=torch.bfloat16, device=dev)
-        _need(grad_hidden, "grad_hidden", torch.bfloat16, tuple(hidden.shape), dev)
-        _need(grad_weight, "grad_weight", torch.bfloat16, (V, D), dev)
-        _check(load().ssd_linear_ce_grad(*args, _ptr(lse), _ptr(row_scale), _ptr(grad_hidden), _ptr(grad_weight),
-                                         _ptr(status), _ptr(ws), ws.numel(), st), "ssd_linear_ce_grad")
-    return grad_hidden, grad_weight
+        gh, gw = grad_hidden, grad_weight
+        if gh is None:
+            gh = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
+        if gw is None:
+            gw = torch.empty((V, D), dtype=torch.bfloat16, device=dev)
+        _check(load().ssd_linear_ce_grad(*args, lse.data_ptr(), _ptr(row_scale), gh.data_ptr(), gw.data_ptr(),
+                                         _ptr(status), ws.data_ptr(), ws.numel(), st), "ssd_linear_ce_grad")
+        return gh, gw
+
+    return _launch(index, stream, call)

@@ -171,16 +171,33 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// mbar_try_wait whose acquire reaches the other CTA of the pair.
+__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  return done != 0;
+}
+
 // A wait of one of the kernel's roles.  Once one has given up, the kernel's
 // other waits in this CTA give up too, and the call is flagged.
+template <int CG>
 struct GemmWait {
   volatile int* abort;
   int32_t* error;
+  static __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+    return CG == 1 ? mbar_try_wait(bar, parity, kSuspendHintNs) : mbar_try_wait_pair(bar, parity);
+  }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
+    if (poll(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     for (uint32_t i = 0; i < (1u << 30); ++i) {
-      if (mbar_try_wait(bar, parity, kSuspendHintNs)) return true;
+      if (poll(bar, parity)) return true;
       if (*abort || global_ns() - t0 > kGemmWaitNs) break;
     }
     *abort = 1;
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     cg::this_cluster().sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const GemmWait wait = {&abort_flag, a.error};
+  const GemmWait<CG> wait = {&abort_flag, a.error};
   const int n_active = a.hdr->n_active;
   const float scale_max = a.hdr->scale_max;
   const GemmWork<Op, CG> work(a, n_active);

@@ -132,6 +132,9 @@ static bool tile_map(CUtensorMap* m, const void* base, bool fp32, long long cols
 
 constexpr int kSmCount = 148;
 constexpr long long kPieceBytes = 128ll << 20;  // of the gradient's logits, kept at a time
+#ifndef SSD_PAIR_N
+#define SSD_PAIR_N 128
+#endif
 constexpr int kMaxSlots = 32;
 
 // Sizes of one call, and where its workspace holds what.
@@ -146,19 +149,26 @@ struct LinearPlan {
 
 static LinearPlan linear_plan(int N, int D, int V, bool grad) {
   LinearPlan p = {};
-  p.cg = 1;
+  p.cg = N > SSD_PAIR_N ? 2 : 1;
   const int tm = 128 * p.cg;
   p.rows = (N + tm - 1) / tm * tm;
   p.tiles = (V + kTileN - 1) / kTileN;
   const long long v_up = static_cast<long long>(p.tiles) * kTileN;
   const long long fit = kPieceBytes / (2ll * p.rows) / kTileN * kTileN;
   p.piece = static_cast<int>(fit < kTileN ? kTileN : (fit > v_up ? v_up : fit));
-  // enough splits to fill the GPU, each of at least 8 blocks of k
-  const int m_tiles = p.rows / tm, d_tiles = (D + kTileN - 1) / kTileN;
-  const int want = (kSmCount / p.cg + m_tiles * d_tiles - 1) / (m_tiles * d_tiles);
+  // Splits of k in dh: the fewest whole waves of tiles per split, each split of
+  // at least 8 blocks of k, few splits where they make no difference.
+  const int m_tiles = p.rows / tm, d_tiles = (D + kTileN - 1) / kTileN, groups = kSmCount / p.cg;
   const int blocks = ((V < p.piece ? V : p.piece) + kBlockK - 1) / kBlockK;
-  const int most = blocks / 8 < 1 ? 1 : (blocks / 8 > kMaxSlots ? kMaxSlots : blocks / 8);
-  p.slots = want < most ? want : most;
+  const long long tiles = static_cast<long long>(m_tiles) * d_tiles;
+  double best = 1e30;
+  for (int k = 1; k <= kMaxSlots && (k == 1 || blocks / k >= 8); ++k) {
+    const double waves = static_cast<double>((tiles * k + groups - 1) / groups) / k * (1.0 + 0.01 * k);
+    if (waves < best) {
+      best = waves;
+      p.slots = k;
+    }
+  }
   size_t off = 0;
   const auto take = [&off](size_t bytes) {
     const size_t at = off;
@@ -414,7 +424,8 @@ ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int 
   a.lse_out = lse;
   a.status = status;
   if ((st = launch_prep(a, s)) != SSD_OK) return st;
-  return linear_forward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, loss, lse, status, s);
+  return p.cg == 1 ? linear_forward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, loss, lse, status, s)
+                   : linear_forward<2>(p, ws, weight, 2ll * weight_stride, N, D, V, loss, lse, status, s);
 }
 
 ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype, int n_batch, int rows_per_batch, int D,
@@ -445,7 +456,9 @@ ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype,
   a.grad_hidden = static_cast<uint16_t*>(grad_hidden);
   a.status = status;
   if ((st = launch_prep(a, s)) != SSD_OK) return st;
-  return linear_backward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, grad_hidden, grad_weight, status, s);
+  return p.cg == 1
+             ? linear_backward<1>(p, ws, weight, 2ll * weight_stride, N, D, V, grad_hidden, grad_weight, status, s)
+             : linear_backward<2>(p, ws, weight, 2ll * weight_stride, N, D, V, grad_hidden, grad_weight, status, s);
 }
 
 }  // extern "C"
