@@ -563,6 +563,8 @@ def _want(t, name: str, dtype, shape, index: int):
         _need(t, name, dtype, shape, torch.device("cuda", index))
 
 
+# (Outputs below are made with empty_like where a tensor of their shape is at
+# hand: 1.3 us each against 3.1 from a torch.Size.)
 # The current stream's handle without a Stream object around it (4 us a call).
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda index: torch.cuda.current_stream(index).cuda_stream
@@ -591,16 +593,15 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -
     e.g. target[:, :K]) with the log-mass of all and of the other tokens (see
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
-    dt, dev, lead = _logit_dtype(logits), logits.device, logits.shape[:-1]
+    dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
     M = int(M)
     wide = lead + (max(M, 0),)
 
     def call(st):
-        r = TeacherTop(tokens=torch.empty(wide, dtype=torch.int32, device=dev),
-                       values=torch.empty(wide, dtype=torch.float32, device=dev),
-                       lse=torch.empty(lead, dtype=torch.float32, device=dev),
-                       tail=torch.empty(lead, dtype=torch.float32, device=dev),
-                       status=torch.empty(lead, dtype=torch.int32, device=dev))
+        values = torch.empty(wide, dtype=torch.float32, device=dev)
+        lse = torch.empty(lead, dtype=torch.float32, device=dev)
+        r = TeacherTop(tokens=torch.empty_like(values, dtype=torch.int32), values=values, lse=lse,
+                       tail=torch.empty_like(lse), status=torch.empty_like(lse, dtype=torch.int32))
         _check(load().ssd_teacher_top(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, r.tokens.data_ptr(),
                                       r.values.data_ptr(), r.lse.data_ptr(), r.tail.data_ptr(), r.status.data_ptr(),
                                       st), "ssd_teacher_top")
@@ -643,12 +644,14 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
     def call(st):
         g = grad
         if with_grad and g is None:
-            g = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            g = torch.empty_like(logits, memory_format=torch.contiguous_format)
             gbs, grs = rpb * V, V
         else:
             gbs, grs = _rows_of(g, "grad")[3:] if with_grad else (0, 0)
-        r = DistillResult(loss=torch.empty(lead, dtype=torch.float32, device=dev),
-                          status=torch.empty(lead, dtype=torch.int32, device=dev), grad=g)
+        known = tail if tail is not None else row_scale
+        loss = torch.empty_like(known) if known is not None else \
+            torch.empty(tuple(lead), dtype=torch.float32, device=dev)
+        r = DistillResult(loss=loss, status=torch.empty_like(loss, dtype=torch.int32), grad=g)
         _check(load().ssd_distill(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, tokens.data_ptr(),
                                   values.data_ptr(), _ptr(tail), _ptr(row_scale), r.loss.data_ptr(),
                                   r.status.data_ptr(), _ptr(g), gbs, grs, st), "ssd_distill")
@@ -703,9 +706,8 @@ def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
 
     def call(st):
         ws = _linear_workspace(workspace, N, D, V, False, dev)
-        r = LinearCeResult(loss=torch.empty(lead, dtype=torch.float32, device=dev),
-                           lse=torch.empty(lead, dtype=torch.float32, device=dev),
-                           status=torch.empty(lead, dtype=torch.int32, device=dev))
+        loss = torch.empty_like(targets, dtype=torch.float32)
+        r = LinearCeResult(loss=loss, lse=torch.empty_like(loss), status=torch.empty_like(targets))
         _check(load().ssd_linear_ce(*args, r.loss.data_ptr(), r.lse.data_ptr(), r.status.data_ptr(), ws.data_ptr(),
                                     ws.numel(), st), "ssd_linear_ce")
         return r
@@ -735,9 +737,9 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
         ws = _linear_workspace(workspace, N, D, V, True, dev)
         gh, gw = grad_hidden, grad_weight
         if gh is None:
-            gh = torch.empty(hidden.shape, dtype=torch.bfloat16, device=dev)
+            gh = torch.empty_like(hidden, memory_format=torch.contiguous_format)
         if gw is None:
-            gw = torch.empty((V, D), dtype=torch.bfloat16, device=dev)
+            gw = torch.empty_like(weight, memory_format=torch.contiguous_format)
         _check(load().ssd_linear_ce_grad(*args, lse.data_ptr(), _ptr(row_scale), gh.data_ptr(), gw.data_ptr(),
                                          _ptr(status), ws.data_ptr(), ws.numel(), st), "ssd_linear_ce_grad")
         return gh, gw

@@ -20,7 +20,7 @@
 namespace ssd {
 
 constexpr int kGemmThreads = 192;  // warp 0: copies, warp 1: products, warps 2-5: epilogue
-constexpr int kTileN = 256;        // accumulator columns
+constexpr int kAccCols = 256;      // TMEM columns of one accumulator
 constexpr int kBlockK = 64;        // one 128-byte swizzle row of bf16
 constexpr int kATile = 128 * kBlockK * 2;
 constexpr int kOutBuf = 32 * 128;  // one epilogue warp's staging buffer: 32 rows of 128 bytes
@@ -28,13 +28,20 @@ constexpr unsigned long long kGemmWaitNs = 2000000000ull;
 
 enum GemmOp { kOpLse = 0, kOpGrad = 1, kOpDh = 2, kOpDw = 3 };
 
-template <int CG>
+// A pair of CTAs (CG = 2) computes 256 x 256 tiles, each CTA staging half of
+// either operand.  A single CTA, for up to 128 rows, where the weight's bytes
+// bound the call, computes tiles of 128 x 128: narrow ones leave less of the
+// last wave idle (64 rows over 128256: 7 waves of 128 columns against 4 of
+// 256).  Its dw tiles, bound by what they write, are 128 x 256: 102 us against
+// 117 there.
+template <int Op, int CG>
 struct GemmShape {
   static constexpr int kTileM = 128 * CG;
+  static constexpr int kTileN = Op == kOpDw ? 256 : 128 * CG;
   static constexpr int kBRows = kTileN / CG;  // the CTA's share of the B tile
   static constexpr int kBTile = kBRows * kBlockK * 2;
   static constexpr int kStage = kATile + kBTile;
-  static constexpr int kStages = CG == 1 ? 4 : 6;
+  static constexpr int kStages = kBRows == 128 ? 6 : 4;
   static constexpr int kSmem = kStages * kStage + 4 * 2 * kOutBuf + 1024;  // and the slack to align to 1 KB
 };
 
@@ -216,14 +223,14 @@ struct GemmWork {
   int m_tiles, n_tiles, k_blocks, count;
   __device__ __forceinline__ GemmWork(const GemmArgs& a, int n_active) {
     const int na = max(n_active, 1);
-    constexpr int TM = GemmShape<CG>::kTileM;
+    constexpr int TM = GemmShape<Op, CG>::kTileM, TN = GemmShape<Op, CG>::kTileN;
     if (Op == kOpDw) {
       m_tiles = (a.v_count + TM - 1) / TM;
-      n_tiles = (a.D + kTileN - 1) / kTileN;
+      n_tiles = (a.D + TN - 1) / TN;
       k_blocks = (na + kBlockK - 1) / kBlockK;
     } else {
       m_tiles = (na + TM - 1) / TM;
-      n_tiles = ((Op == kOpDh ? a.D : a.v_count) + kTileN - 1) / kTileN;
+      n_tiles = ((Op == kOpDh ? a.D : a.v_count) + TN - 1) / TN;
       k_blocks = ((Op == kOpDh ? a.v_count : a.D) + kBlockK - 1) / kBlockK;
     }
     count = m_tiles * n_tiles * (Op == kOpDh ? a.slots : 1);
@@ -241,6 +248,7 @@ struct GemmWork {
         r.slot = t / (m_tiles * n_tiles);
         t -= r.slot * m_tiles * n_tiles;
       }
+      if (Op == kOpGrad) t = count - 1 - t;  // the forward call went upwards: its last weights may be in L2
       r.m = t % m_tiles;
       r.n = t / m_tiles;
     }
@@ -275,8 +283,8 @@ template <int Op, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     ssd_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_out, const GemmArgs a) {
-  using S = GemmShape<CG>;
-  constexpr int kStages = S::kStages;
+  using S = GemmShape<Op, CG>;
+  constexpr int kStages = S::kStages, kTileN = S::kTileN;
   constexpr bool kAMn = Op == kOpDw, kBMn = Op == kOpDh || Op == kOpDw;
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (tile.kb0 == tile.kb1) continue;
         if (!wait(&tempty[acc], acc_phase ^ 1)) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * kTileN;
+        const uint32_t d = tmem + acc * kAccCols;
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
           if (!wait(&full[s], phase)) {
             ok = false;
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int n_valid = a.v_count - tile.n * kTileN;  // lse, grad: columns inside the vocabulary
       if (!wait(&tfull[acc], acc_phase)) break;
       tc_fence_after();
-      const uint32_t src = tmem + acc * kTileN + (static_cast<uint32_t>(quad * 32) << 16);
+      const uint32_t src = tmem + acc * kAccCols + (static_cast<uint32_t>(quad * 32) << 16);
       float mx = -INFINITY, sum = 0.f;
 #pragma unroll 1
       for (int c = 0; c < kTileN / 32; ++c) {
@@ -636,7 +644,12 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
           static_cast<const uint16_t*>(a.hidden.base) +
           row_offset(a.hidden.batch_stride, a.hidden.row_stride, a.hidden.rows_per_batch, n0 + i));
       uint4* dst = reinterpret_cast<uint4*>(a.h + static_cast<size_t>(at) * a.D);
-      for (int v = lane; v < vecs; v += 32) dst[v] = src[v];
+      int v = lane;
+      for (; v + 96 < vecs; v += 128) {  // four loads in flight
+        const uint4 x0 = __ldg(src + v), x1 = __ldg(src + v + 32), x2 = __ldg(src + v + 64), x3 = __ldg(src + v + 96);
+        dst[v] = x0, dst[v + 32] = x1, dst[v + 64] = x2, dst[v + 96] = x3;
+      }
+      for (; v < vecs; v += 32) dst[v] = __ldg(src + v);
     } else if (a.grad_hidden) {
       uint4* dst = reinterpret_cast<uint4*>(a.grad_hidden + static_cast<size_t>(n0 + i) * a.D);
       for (int v = lane; v < vecs; v += 32) dst[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -651,45 +664,73 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
   }
 }
 
-constexpr int kJoinThreads = 1024;  // 32 rows of 32 warps
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinRows = 8;  // of one block: 128 threads share a row's tiles
 
-// Joins the vocabulary tiles' maxima and sums: a lane per row, the warps share
-// the tiles, in a fixed order.
+// (maximum, sum of exponentials around it), joined.
+struct MaxSum {
+  float max;
+  double sum;
+};
+__device__ __forceinline__ MaxSum join(const MaxSum& a, const MaxSum& b) {
+  const float m = fmaxf(a.max, b.max);
+  const float ref = m > -INFINITY ? m : 0.f;
+  return MaxSum{m, a.sum * static_cast<double>(ex2((a.max - ref) * kLog2e)) +
+                       b.sum * static_cast<double>(ex2((b.max - ref) * kLog2e))};
+}
+
+// Joins the vocabulary tiles' maxima and sums, in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads)
     ssd_linear_join_kernel(const LinearHdr* hdr, const float2* part, int rows, int tiles, const int32_t* index,
                            const float* zt, float* loss, float* lse, int32_t* status) {
-  __shared__ float maxima[32][33];
-  __shared__ double sums[32][33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = static_cast<int>(blockIdx.x) * 32 + lane;
+  __shared__ float maxima[32][kJoinRows];
+  __shared__ double sums[32][kJoinRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = tid % kJoinRows;
+  const int row0 = static_cast<int>(blockIdx.x) * kJoinRows, row = row0 + r;
   const int n_active = hdr->n_active;
-  if (static_cast<int>(blockIdx.x) * 32 >= n_active) return;
+  if (row0 >= n_active) return;
   const bool live = row < n_active;
-  float mx = -INFINITY;
-  double sum = 0.0;
-  if (live) {
-#pragma unroll 4
-    for (int t = warp; t < tiles; t += 32) {
-      const float2 p = part[static_cast<size_t>(t) * rows + row];
-      const float m = fmaxf(mx, p.x);
-      const float ref = m > -INFINITY ? m : 0.f;
-      sum = sum * static_cast<double>(ex2((mx - ref) * kLog2e)) +
-            static_cast<double>(p.y) * static_cast<double>(ex2((p.x - ref) * kLog2e));
-      mx = m;
-    }
-  }
-  maxima[warp][lane] = mx;
-  sums[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && live) {
+  MaxSum s = {-INFINITY, 0.0};
+  constexpr int kStep = kJoinThreads / kJoinRows, kBatch = 8;  // loads in flight
+  for (int t0 = tid / kJoinRows; live && t0 < tiles; t0 += kStep * kBatch) {
+    float2 p[kBatch];
     float m = -INFINITY;
-    for (int w = 0; w < 32; ++w) m = fmaxf(m, maxima[w][lane]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t = t0 + i * kStep;
+      p[i] = t < tiles ? part[static_cast<size_t>(t) * rows + row] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) m = fmaxf(m, p[i].x);
     const float ref = m > -INFINITY ? m : 0.f;
-    double s = 0.0;
-    for (int w = 0; w < 32; ++w) s += sums[w][lane] * static_cast<double>(ex2((maxima[w][lane] - ref) * kLog2e));
-    const double l = static_cast<double>(ref) + log(s);
-    const int n = index[row];
-    const double z = static_cast<double>(zt[row]);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) sum += p[i].y * ex2((p[i].x - ref) * kLog2e);
+    s = join(s, MaxSum{m, static_cast<double>(sum)});
+  }
+#pragma unroll
+  for (int o = kJoinRows; o < 32; o <<= 1) {
+    const MaxSum q = {__shfl_down_sync(0xFFFFFFFFu, s.max, o), __shfl_down_sync(0xFFFFFFFFu, s.sum, o)};
+    s = join(s, q);
+  }
+  if (lane < kJoinRows) {
+    maxima[warp][lane] = s.max;
+    sums[warp][lane] = s.sum;
+  }
+  __syncthreads();
+  if (warp >= kJoinRows) return;
+  // a warp per row: lane w holds warp w's
+  s = MaxSum{maxima[lane][warp], sums[lane][warp]};
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const MaxSum q = {__shfl_down_sync(0xFFFFFFFFu, s.max, o), __shfl_down_sync(0xFFFFFFFFu, s.sum, o)};
+    s = join(s, q);
+  }
+  const int at = row0 + warp;
+  if (lane == 0 && at < n_active) {
+    const double l = static_cast<double>(s.max > -INFINITY ? s.max : 0.f) + log(s.sum);
+    const int n = index[at];
+    const double z = static_cast<double>(zt[at]);
     int32_t st = 0;
     if (!(fabs(l) < INFINITY) || !(fabs(z) < INFINITY)) st |= SSD_ROW_NONFINITE;
     if (hdr->error) st |= SSD_ROW_DEVICE_TIMEOUT;

@@ -35,10 +35,7 @@ static cudaError_t allow_smem(const void* fn, int bytes) {
 // ---------------------------------------------------------------------------
 // Rows in cluster shared memory.
 // ---------------------------------------------------------------------------
-#ifndef SSD_SLICE
-#define SSD_SLICE 52
-#endif
-constexpr long long kSliceTarget = SSD_SLICE * 1024;  // bytes of a row that one CTA stages: three CTAs fit an SM
+constexpr long long kSliceTarget = 52 * 1024;  // bytes of a row that one CTA stages: four CTAs fit an SM
 constexpr long long kSliceMin = 8 * 1024;      // do not split a row finer than this for the sake of few rows
 constexpr long long kSliceMax = 200 * 1024;
 constexpr int kRowFill = 2 * 148;              // CTAs that fill the GPU
@@ -131,10 +128,7 @@ static bool tile_map(CUtensorMap* m, const void* base, bool fp32, long long cols
 }
 
 constexpr int kSmCount = 148;
-constexpr long long kPieceBytes = 128ll << 20;  // of the gradient's logits, kept at a time
-#ifndef SSD_PAIR_N
-#define SSD_PAIR_N 128
-#endif
+constexpr long long kPieceBytes = 256ll << 20;  // of the gradient's logits, kept at a time
 constexpr int kMaxSlots = 32;
 
 // Sizes of one call, and where its workspace holds what.
@@ -149,16 +143,16 @@ struct LinearPlan {
 
 static LinearPlan linear_plan(int N, int D, int V, bool grad) {
   LinearPlan p = {};
-  p.cg = N > SSD_PAIR_N ? 2 : 1;
-  const int tm = 128 * p.cg;
+  p.cg = N > 128 ? 2 : 1;
+  const int tm = 128 * p.cg, tn = tm;
   p.rows = (N + tm - 1) / tm * tm;
-  p.tiles = (V + kTileN - 1) / kTileN;
-  const long long v_up = static_cast<long long>(p.tiles) * kTileN;
-  const long long fit = kPieceBytes / (2ll * p.rows) / kTileN * kTileN;
-  p.piece = static_cast<int>(fit < kTileN ? kTileN : (fit > v_up ? v_up : fit));
+  p.tiles = (V + tn - 1) / tn;
+  const long long v_up = (V + 255ll) / 256 * 256;  // dw's tiles are 256 high
+  const long long fit = kPieceBytes / (2ll * p.rows) / 256 * 256;
+  p.piece = static_cast<int>(fit < 256 ? 256 : (fit > v_up ? v_up : fit));
   // Splits of k in dh: the fewest whole waves of tiles per split, each split of
   // at least 8 blocks of k, few splits where they make no difference.
-  const int m_tiles = p.rows / tm, d_tiles = (D + kTileN - 1) / kTileN, groups = kSmCount / p.cg;
+  const int m_tiles = p.rows / tm, d_tiles = (D + tn - 1) / tn, groups = kSmCount / p.cg;
   const int blocks = ((V < p.piece ? V : p.piece) + kBlockK - 1) / kBlockK;
   const long long tiles = static_cast<long long>(m_tiles) * d_tiles;
   double best = 1e30;
@@ -197,13 +191,13 @@ template <int Op, int CG>
 static ssd_status launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a,
                               long long most_tiles, cudaStream_t stream) {
   const auto fn = &ssd_gemm_kernel<Op, CG>;
-  if (allow_smem(reinterpret_cast<const void*>(fn), GemmShape<CG>::kSmem) != cudaSuccess) return SSD_ERR_CUDA;
+  if (allow_smem(reinterpret_cast<const void*>(fn), GemmShape<Op, CG>::kSmem) != cudaSuccess) return SSD_ERR_CUDA;
   const long long fit = kSmCount / CG;
   const long long groups = most_tiles < fit ? most_tiles : fit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
   cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = GemmShape<CG>::kSmem;
+  cfg.dynamicSmemBytes = GemmShape<Op, CG>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -268,17 +262,17 @@ template <int CG>
 static ssd_status linear_forward(const LinearPlan& p, char* ws, const void* weight, long long ws_bytes_row, int N, int D,
                                  int V, float* loss, float* lse, int32_t* status, cudaStream_t stream) {
   CUtensorMap mh, mw;
-  if (!tile_map(&mh, ws + p.h, false, D, p.rows, 2ll * D, 128) ||
-      !tile_map(&mw, weight, false, D, V, ws_bytes_row, GemmShape<CG>::kBRows))
+  if (!tile_map(&mh, ws + p.h, false, D, N, 2ll * D, 128) ||
+      !tile_map(&mw, weight, false, D, V, ws_bytes_row, GemmShape<kOpLse, CG>::kBRows))
     return SSD_ERR_CUDA;
   GemmArgs g = gemm_args(p, ws, V, D);
   g.v_count = V;
   g.zt = reinterpret_cast<float*>(ws + p.zt);
   g.part = reinterpret_cast<float2*>(ws + p.part);
-  const long long most = static_cast<long long>(p.rows / (128 * CG)) * p.tiles;
+  const long long most = static_cast<long long>(p.rows / GemmShape<kOpLse, CG>::kTileM) * p.tiles;
   const ssd_status st = launch_gemm<kOpLse, CG>(mh, mw, mw, g, most, stream);
   if (st != SSD_OK) return st;
-  ssd_linear_join_kernel<<<(N + 31) / 32, kJoinThreads, 0, stream>>>(
+  ssd_linear_join_kernel<<<(N + kJoinRows - 1) / kJoinRows, kJoinThreads, 0, stream>>>(
       g.hdr, g.part, p.rows, p.tiles, reinterpret_cast<const int32_t*>(ws + p.index), g.zt, loss, lse, status);
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -287,15 +281,17 @@ template <int CG>
 static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* weight, long long ws_bytes_row, int N,
                                   int D, int V, void* grad_hidden, void* grad_weight, int32_t* status,
                                   cudaStream_t stream) {
-  using S = GemmShape<CG>;
+  using S = GemmShape<kOpGrad, CG>;
+  using W = GemmShape<kOpDw, CG>;
   CUtensorMap h_k, h_mn, w_k, w_mn, g_out, g_k, g_mn, dh_out, dw_out;
-  if (!tile_map(&h_k, ws + p.h, false, D, p.rows, 2ll * D, 128) ||
-      !tile_map(&h_mn, ws + p.h, false, D, p.rows, 2ll * D, 64) ||
+  // The maps end at row N: what a tile reads behind it is zero and costs no traffic.
+  if (!tile_map(&h_k, ws + p.h, false, D, N, 2ll * D, 128) ||
+      !tile_map(&h_mn, ws + p.h, false, D, N, 2ll * D, 64) ||
       !tile_map(&w_k, weight, false, D, V, ws_bytes_row, S::kBRows) ||
       !tile_map(&w_mn, weight, false, D, V, ws_bytes_row, 64) ||
-      !tile_map(&g_out, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 32) ||
-      !tile_map(&g_k, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 128) ||
-      !tile_map(&g_mn, ws + p.g, false, p.piece, p.rows, 2ll * p.piece, 64) ||
+      !tile_map(&g_out, ws + p.g, false, p.piece, N, 2ll * p.piece, 32) ||
+      !tile_map(&g_k, ws + p.g, false, p.piece, N, 2ll * p.piece, 128) ||
+      !tile_map(&g_mn, ws + p.g, false, p.piece, N, 2ll * p.piece, 64) ||
       !tile_map(&dh_out, ws + p.dh, true, D, static_cast<long long>(p.rows) * p.slots, 4ll * D, 32) ||
       !tile_map(&dw_out, grad_weight, false, D, V, 2ll * D, 32))
     return SSD_ERR_CUDA;
@@ -303,16 +299,17 @@ static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* wei
   g.scale = reinterpret_cast<const float*>(ws + p.scale);
   g.lse = reinterpret_cast<const float*>(ws + p.lse);
   g.slots = p.slots;
-  const long long m_tiles = p.rows / S::kTileM, d_tiles = (D + kTileN - 1) / kTileN;
+  const long long m_tiles = p.rows / S::kTileM, d_tiles = (D + S::kTileN - 1) / S::kTileN;
   for (long long v0 = 0; v0 < V; v0 += p.piece) {
     g.v0 = static_cast<int>(v0);
     g.v_count = static_cast<int>(V - v0 < p.piece ? V - v0 : p.piece);
     g.first = v0 == 0;
-    const long long v_tiles = (g.v_count + kTileN - 1) / kTileN;
+    const long long v_tiles = (g.v_count + S::kTileN - 1) / S::kTileN;
     ssd_status st = launch_gemm<kOpGrad, CG>(h_k, w_k, g_out, g, m_tiles * v_tiles, stream);
     if (st == SSD_OK) st = launch_gemm<kOpDh, CG>(g_k, w_mn, dh_out, g, m_tiles * d_tiles * p.slots, stream);
     if (st == SSD_OK)
-      st = launch_gemm<kOpDw, CG>(g_mn, h_mn, dw_out, g, (g.v_count + S::kTileM - 1) / S::kTileM * d_tiles, stream);
+      st = launch_gemm<kOpDw, CG>(g_mn, h_mn, dw_out, g,
+                                   (g.v_count + W::kTileM - 1ll) / W::kTileM * ((D + W::kTileN - 1) / W::kTileN), stream);
     if (st != SSD_OK) return st;
   }
   const dim3 grid(static_cast<unsigned>(N), static_cast<unsigned>((D / 4 + kDhThreads - 1) / kDhThreads));
