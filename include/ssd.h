@@ -355,8 +355,9 @@ ssd_status ssd_cache_lookup(const int32_t* offsets, const int32_t* tokens, int B
  * j * row_stride, tokens are adjacent, and rows may start at any element (no
  * 16-byte rule).  So the K draft positions of target logits [B, K+1, V] are
  * (B, K, V) with batch_stride (K+1) V; other per-row arrays are dense, row
- * b * rows_per_batch + j.  One cluster of thread blocks stages a whole row in
- * shared memory: rows of up to 1.6 MB (V <= 400000 fp32, 800000 bf16), else
+ * b * rows_per_batch + j.  ssd_distill stages a whole row in the shared memory
+ * of one cluster of thread blocks: rows of up to 1.6 MB (V <= 400000 fp32,
+ * 800000 bf16); ssd_teacher_top takes four times that.  Larger rows:
  * SSD_ERR_UNSUPPORTED.  SSD_MIN_TRAIN_T <= T <= SSD_MAX_TRAIN_T.  Results are
  * the same bits on every call with the same inputs at the same alignment
  * (modulo 16 bytes) and number of rows.
@@ -370,10 +371,18 @@ ssd_status ssd_cache_lookup(const int32_t* offsets, const int32_t* tokens, int B
  *   not among the M (-inf when there are none), formed without subtraction.
  *   1 <= M <= min(V, SSD_MAX_TOP).  status [rows] out: SSD_ROW_NONFINITE for a
  *   row with a NaN or +inf logit or all of -inf (tokens -1, the rest NaN).
+ *   workspace: ssd_teacher_top_workspace_bytes() bytes, 256-byte aligned; it
+ *   needs no initial contents, and calls that overlap on the GPU must not
+ *   share one.
  */
 ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_per_batch, int V,
                            int64_t batch_stride, int64_t row_stride, float T, int M, int32_t* tokens,
-                           float* values, float* lse, float* tail, int32_t* status, void* stream);
+                           float* values, float* lse, float* tail, int32_t* status, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Workspace size of ssd_teacher_top for `rows` rows in all; 0 where it needs
+ * none (workspace may then be NULL) and for invalid sizes. */
+size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
 
 /*
  * ssd_distill -- distillation loss of student rows z against a teacher of M

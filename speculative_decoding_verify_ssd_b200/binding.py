@@ -102,7 +102,9 @@ def load(build_if_missing: bool = True):
     L.ssd_cache_lookup.restype = i32
     L.ssd_cache_lookup.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, C.c_uint64, i32, vp, vp, vp, vp]
     L.ssd_teacher_top.restype = i32
-    L.ssd_teacher_top.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp]
+    L.ssd_teacher_top.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.ssd_teacher_top_workspace_bytes.restype = sz
+    L.ssd_teacher_top_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.ssd_distill.restype = i32
     L.ssd_distill.argtypes = [vp, i32, i32, i32, i32, i64, i64, f32, i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp]
     L.ssd_linear_ce_workspace_bytes.restype = sz
@@ -588,7 +590,22 @@ class TeacherTop:
     status: torch.Tensor
 
 
-def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -> TeacherTop:
+def _scratch(workspace, nbytes: int, dev):
+    """The caller's workspace (a uint8 tensor), or one of the caching allocator:
+    it belongs to the current stream, or to the graph that is being captured."""
+    if workspace is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense torch.uint8 tensor on {dev}")
+    return workspace
+
+
+def teacher_top_workspace_bytes(rows: int, V: int, dtype: int, M: int) -> int:
+    return int(load().ssd_teacher_top_workspace_bytes(rows, V, dtype, M))
+
+
+def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> TeacherTop:
     """Top-M logits of every row of `logits` ([..., V], up to three dimensions,
     e.g. target[:, :K]) with the log-mass of all and of the other tokens (see
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
@@ -598,13 +615,14 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, stream=None) -
     wide = lead + (max(M, 0),)
 
     def call(st):
+        ws = _scratch(workspace, load().ssd_teacher_top_workspace_bytes(nb * rpb, V, dt, M), dev)
         values = torch.empty(wide, dtype=torch.float32, device=dev)
         lse = torch.empty(lead, dtype=torch.float32, device=dev)
         r = TeacherTop(tokens=torch.empty_like(values, dtype=torch.int32), values=values, lse=lse,
                        tail=torch.empty_like(lse), status=torch.empty_like(lse, dtype=torch.int32))
         _check(load().ssd_teacher_top(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, r.tokens.data_ptr(),
                                       r.values.data_ptr(), r.lse.data_ptr(), r.tail.data_ptr(), r.status.data_ptr(),
-                                      st), "ssd_teacher_top")
+                                      _ptr(ws), 0 if ws is None else ws.numel(), st), "ssd_teacher_top")
         return r
 
     return _launch(dev.index, stream, call)
@@ -680,16 +698,6 @@ def _linear_args(hidden, weight, targets):
                                        weight.stride(0) if V > 1 else max(weight.stride(0), D), targets.data_ptr())
 
 
-def _linear_workspace(workspace, N, D, V, grad, dev):
-    """The caller's workspace (a uint8 tensor), or one of the caching allocator:
-    it belongs to the current stream, or to the graph that is being captured."""
-    if workspace is None:
-        return torch.empty(max(linear_ce_workspace_bytes(N, D, V, grad), 1), dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a dense torch.uint8 tensor on {dev}")
-    return workspace
-
-
 @dataclass
 class LinearCeResult:
     loss: torch.Tensor
@@ -705,7 +713,7 @@ def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     dev, lead, N, D, V, args = _linear_args(hidden, weight, targets)
 
     def call(st):
-        ws = _linear_workspace(workspace, N, D, V, False, dev)
+        ws = _scratch(workspace, max(linear_ce_workspace_bytes(N, D, V, False), 1), dev)
         loss = torch.empty_like(targets, dtype=torch.float32)
         r = LinearCeResult(loss=loss, lse=torch.empty_like(loss), status=torch.empty_like(targets))
         _check(load().ssd_linear_ce(*args, r.loss.data_ptr(), r.lse.data_ptr(), r.status.data_ptr(), ws.data_ptr(),
@@ -734,7 +742,7 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
         _want(grad_weight, "grad_weight", torch.bfloat16, (V, D), index)
 
     def call(st):
-        ws = _linear_workspace(workspace, N, D, V, True, dev)
+        ws = _scratch(workspace, max(linear_ce_workspace_bytes(N, D, V, True), 1), dev)
         gh, gw = grad_hidden, grad_weight
         if gh is None:
             gh = torch.empty_like(hidden, memory_format=torch.contiguous_format)

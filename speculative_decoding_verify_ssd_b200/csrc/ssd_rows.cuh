@@ -1,9 +1,11 @@
 // ssd_rows.cuh -- the vocabulary-row operators of draft training: the top
 // logits of a row with the mass left outside them (ssd_teacher_top) and the
 // distillation loss of a row against such a teacher with its gradient
-// (ssd_distill).  One thread-block cluster holds one whole row in its CTAs'
-// shared memory, so a row is read from HBM once however many passes the
-// arithmetic takes over it.
+// (ssd_distill).  A CTA stages a slice of a row in shared memory, so a row is
+// read from HBM once however many passes the arithmetic takes over it.  The
+// distillation, whose gradient needs the whole row's sums, holds the row in one
+// thread-block cluster; the top logits of the slices are joined by a second,
+// small kernel.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -18,7 +20,7 @@ namespace ssd {
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxRowCluster = 8;   // the portable cluster size
-constexpr int kPool = 448;          // top candidates ranked at once
+constexpr int kPool = 448;          // top candidates ranked at once (even)
 constexpr unsigned long long kRowWaitNs = 1000000000ull;  // limit of the wait for a slice's bytes
 
 // Rows of a [n_batch, rows_per_batch, V] tensor, strides in elements.
@@ -145,12 +147,16 @@ __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s
   }
 }
 
-// Waits for the slice's bytes.  A wait that gives up waits once more (the
-// copies still target this CTA's shared memory) before the row is flagged.
+// Waits for the slice's bytes; a barrier of the CTA (one warp polls, the others
+// stand at the barrier).  A wait that gives up waits once more (the copies still
+// target this CTA's shared memory) before the row is flagged.
 __device__ __forceinline__ int slice_wait(uint64_t* bar, uint32_t parity) {
-  if (mbar_wait_bounded(bar, parity, kRowWaitNs)) return 0;
-  (void)mbar_wait_bounded(bar, parity, kRowWaitNs);
-  return SSD_ROW_DEVICE_TIMEOUT;
+  int late = 0;
+  if (threadIdx.x >= kRowThreads - 32) {
+    late = mbar_wait_bounded(bar, parity, kRowWaitNs) ? 0 : SSD_ROW_DEVICE_TIMEOUT;
+    if (late) (void)mbar_wait_bounded(bar, parity, kRowWaitNs);
+  }
+  return __syncthreads_or(late) ? SSD_ROW_DEVICE_TIMEOUT : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -392,6 +398,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     return;
   }
 
+  cluster.barrier_arrive();  // this CTA runs: the others may write into it
   if (warp == kRowWarps - 1) {
     if (lane == 0) {
       mbar_init(&bar, 1);
@@ -471,6 +478,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     if (lane == 0) warps[warp] = DistillPart{ref, sum, am, as, num, weight, flags};
   }
   __syncthreads();
+  cluster.barrier_wait();  // every CTA runs
   if (warp == 0) {
     // The CTA's part, written into every CTA of the cluster (its loss terms
     // only into the first): a few remote stores, and after the barrier every
@@ -580,7 +588,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
 }
 
 // ---------------------------------------------------------------------------
-// The top M logits of a row.
+// The top M logits of a row.  Each CTA lists the logits of its slice that can
+// be among them (all at or above a threshold that at least M reach), and sums
+// the exponentials of the others; a row of one slice is then done, else the
+// join kernel ranks the slices' lists.  (One cluster per row, exchanging over
+// distributed shared memory, took 54 us for 384 rows of 128256 bf16: its CTAs
+// waited for one another three times a row.)
 // ---------------------------------------------------------------------------
 struct TopArgs {
   RowsIn in;
@@ -589,50 +602,29 @@ struct TopArgs {
   float* lse;       // [rows]
   float* tail;      // [rows]
   int32_t* status;  // [rows]
-  int V, M, slice_vecs;
-  double inv_t;   // 1 / T
-  float log2e_t;  // log2(e) / T
+  struct TopSlice* slices;       // [rows, n_slices]
+  unsigned long long* keys;      // [rows, n_slices, kPool]
+  int V, M, slice_vecs, n_slices;
+  double inv_t;
+  float log2e_t;
 };
 
-// A thread's two largest vectors by their largest element, and where the first
-// of them is: few threads need to look at more than that one for candidates.
-struct TwoMax {
-  float first, second;  // NaN in the second when any element is
-  int at;
-};
-template <typename TIn>
-__device__ __forceinline__ TwoMax slice_two_max(const uint4* data, int count) {
-  TwoMax m = {-INFINITY, -INFINITY, static_cast<int>(threadIdx.x)};
-#pragma unroll 2
-  for (int i = threadIdx.x; i < count; i += kRowThreads) {
-    const float v = Elem<TIn>::vec_max(data[i]);
-    if (v > m.first) {
-      m.second = fmax_nan(m.second, m.first);
-      m.first = v;
-      m.at = i;
-    } else {
-      m.second = fmax_nan(m.second, v);
-    }
-  }
-  return m;
-}
-
-// What a CTA of a row tells the others: the sum of its exponentials outside the
-// candidates, and how many candidates it has.
-struct TopPart {
+// What one slice found: the largest key (which tells NaN and +inf), how many
+// keys it lists, the 16 high bits of a key that M of them reach (0: of none),
+// and the sum of the exponentials of its other logits around ref.
+struct TopSlice {
   double sum;
+  float ref;
+  uint32_t top, cut;
   int count, timeout;
 };
 
-// Rank 0 orders the candidates where its slice was staged.
-constexpr int kTopMinBytes = kPool * sizeof(float);
-
-// The row's maxima over groups of threads, at most kMaxima of them: their M-th
-// largest is a lower bound of the row's M-th largest logit, and few logits
-// reach it.
-constexpr int kMaxima = 512;
+// Maxima of a slice: every thread's largest vector maximum, and for larger M its
+// second largest too.  Their M-th largest is a lower bound of the slice's M-th
+// largest logit, and few logits reach it.
+constexpr int kMaxima = 2 * kRowThreads;
+static_assert(kPool % 2 == 0 && kPool * sizeof(uint16_t) <= kMaxima * sizeof(uint32_t), "the maxima's place holds the vectors'");
 static_assert(kMaxima >= 2 * SSD_MAX_TOP && kPool > SSD_MAX_TOP, "more maxima and places than logits asked for");
-constexpr uint32_t kKeyTimeout = 0xFFFFFFFEu;  // stands for a slice that did not arrive; a NaN's key is 0xFFFFFFFF
 
 // The key of a logit from its kKeyBits high bits: the bits below them are the
 // complement of the mantissa's zeros in a negative logit's key.
@@ -648,12 +640,12 @@ __device__ __forceinline__ uint32_t full_key(uint32_t k) {
 // of few instructions: a search of all 16 bits took 3600 cycles, and 5900
 // unrolled, since straight-line code waits for its instructions.
 template <int kPerLane>
-__device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int n, int M) {
+__device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int M) {
   const int lane = threadIdx.x & 31;
   uint32_t keys[kPerLane], top = 0u, low = 0xFFFFFFFFu;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
-    keys[i] = i * 32 + lane < n ? all[i * 32 + lane] : 0u;
+    keys[i] = all[i * 32 + lane];
     top = max(top, keys[i]);
     low = min(low, keys[i]);
     keys[i] >>= 16;
@@ -661,9 +653,8 @@ __device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int n, i
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   low = __reduce_min_sync(0xFFFFFFFFu, low) >> 16;
   uint32_t high = (top >> 16) + 1u;  // fewer than M reach `high`, at least M reach `low`
-  if (n < M) low = 0u;
 #pragma unroll 1
-  while (high - low > 1u && n >= M) {
+  while (high - low > 1u) {
     const uint32_t d = high - low, m1 = low + (d + 3) / 4, m2 = low + (d + 1) / 2, m3 = low + (3 * d + 3) / 4;
     uint32_t k = 0u;  // three counts of at most kMaxima
 #pragma unroll
@@ -688,30 +679,219 @@ __device__ __forceinline__ uint2 threshold_and_top(const uint32_t* all, int n, i
   return make_uint2(low << 16, top);
 }
 
+// A thread's largest vectors by their largest element, and where the first two
+// are: few threads hold more than two vectors with candidates.
+struct TopVecs {
+  float first, second, third;  // NaN in the third when any element is
+  int at, at2;
+};
+template <typename TIn>
+__device__ __forceinline__ TopVecs slice_top_vecs(const uint4* data, int count) {
+  TopVecs m = {-INFINITY, -INFINITY, -INFINITY, 0, 0};
+#pragma unroll 2
+  for (int i = threadIdx.x; i < count; i += kRowThreads) {
+    const float v = Elem<TIn>::vec_max(data[i]);
+    if (v > m.second) {
+      m.third = fmax_nan(m.third, m.second);
+      const bool best = v > m.first;
+      m.second = best ? m.first : v;
+      m.at2 = best ? m.at : i;
+      m.first = best ? v : m.first;
+      m.at = best ? i : m.at;
+    } else {
+      m.third = fmax_nan(m.third, v);
+    }
+  }
+  return m;
+}
+
+__device__ __forceinline__ int key_token(unsigned long long k) {
+  return static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k & 0xFFFFFFFFull));
+}
+__device__ __forceinline__ float key_logit(unsigned long long k) { return key_to_float(static_cast<uint32_t>(k >> 32)); }
+
+// Outputs of a row that cannot be ranked.
+__device__ __forceinline__ void top_void(const TopArgs& a, int row, int status) {
+  for (int i = threadIdx.x; i < a.M; i += kRowThreads) {
+    a.tokens[static_cast<long long>(row) * a.M + i] = -1;
+    a.values[static_cast<long long>(row) * a.M + i] = __int_as_float(0x7FC00000);
+  }
+  if (threadIdx.x == 0) {
+    a.lse[row] = a.tail[row] = __int_as_float(0x7FC00000);
+    a.status[row] = status;
+  }
+}
+
+// lse and tail of a row from the sum of the top's exponentials around the row's
+// largest logit and the others' around ref.  One warp.
+__device__ __forceinline__ void top_logs(const TopArgs& a, int row, float row_max, double top_sum, float ref,
+                                         double others) {
+  const double share = others > 0.0 ? others * static_cast<double>(ex2((ref - row_max) * a.log2e_t)) : 0.0;
+  const int lane = threadIdx.x & 31;
+  const double logs = log(lane == 0 ? others : top_sum + share);  // two logarithms at once
+  if (lane == 0) {
+    a.tail[row] = others > 0.0 ? static_cast<float>(static_cast<double>(ref) * a.inv_t + logs) : -INFINITY;
+    a.status[row] = 0;
+  }
+  if (lane == 1) a.lse[row] = static_cast<float>(static_cast<double>(row_max) * a.inv_t + logs);
+}
+
+constexpr int kMaxTopSlices = 16;
+constexpr int kShort = 512;  // keys of a row that are ranked from a list of their own (even)
+
+// Shared memory of top_finish.
+struct TopFinish {
+  TopSlice slices[kMaxTopSlices];
+  __align__(16) unsigned long long list[kShort];
+  float ranked[SSD_MAX_TOP];
+  float fred[kRowWarps];
+  double dred[kRowWarps];
+  unsigned long long ured[kRowWarps], last;
+  int n_list;
+};
+
+// The outputs of a row from its n listed keys (with a 0 behind them: 0 is below
+// every key) and its slices' sums.  Whatever order the keys stand in, the
+// results are the same bits: ranks are exact, the top's sum runs over the ranks,
+// and the other listed ones are summed in integers.
+__device__ __forceinline__ void top_finish(const TopArgs& a, int row, unsigned long long* keys, int n, int S,
+                                           TopFinish& f) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float c = a.log2e_t;
+  if (tid == 0) f.n_list = 0;
+  __syncthreads();
+  uint32_t top = 0u;
+  int timeout = 0;
+  float ref = -INFINITY;
+  for (int s = 0; s < S; ++s) {
+    top = max(top, f.slices[s].top);
+    timeout |= f.slices[s].timeout;
+    if (f.slices[s].sum > 0.0) ref = fmaxf(ref, f.slices[s].ref);
+  }
+  if (timeout || top >= ord_key(INFINITY) || top <= ord_key(-INFINITY)) {
+    top_void(a, row, timeout ? SSD_ROW_DEVICE_TIMEOUT : SSD_ROW_NONFINITE);
+    return;
+  }
+  const float row_max = key_to_float(top);
+
+  // A cut at 16 bits that at least M keys reach, and not many more, by halving
+  // from the slices' largest threshold: the barrier counts.
+  const uint32_t* high = reinterpret_cast<const uint32_t*>(keys) + 1;  // the logit's half of a key
+  uint32_t lo = 0u, hi = (top >> 16) + 1u;
+  for (int s = 0; s < S; ++s) lo = max(lo, f.slices[s].cut);
+  const uint32_t k0 = tid < n ? high[2 * tid] >> 16 : 0u, k1 = tid + kRowThreads < n ? high[2 * (tid + kRowThreads)] >> 16 : 0u;
+#pragma unroll 1
+  while (hi - lo > 1u) {
+    const uint32_t mid = (lo + hi) >> 1;
+    int k = __syncthreads_count(k0 >= mid);
+    if (n > kRowThreads) k += __syncthreads_count(k1 >= mid);
+    for (int i0 = 2 * kRowThreads; i0 < n; i0 += kRowThreads)
+      k += __syncthreads_count(i0 + tid < n && (high[2 * (i0 + tid)] >> 16) >= mid);
+    if (k >= a.M) {
+      lo = mid;
+      if (k <= a.M + a.M / 4 + 4) break;
+    } else {
+      hi = mid;
+    }
+  }
+  const uint32_t cut = lo << 16;
+  for (int i0 = warp * 32; i0 < n; i0 += kRowThreads) {
+    const int i = i0 + lane;
+    const bool on = i < n && high[2 * i] >= cut;
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+    int at = 0;
+    if (lane == 0 && who) at = atomicAdd(&f.n_list, __popc(who));
+    at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
+    if (on && at < kShort) f.list[at] = keys[i];
+  }
+  __syncthreads();
+  const bool fits = f.n_list < kShort;
+  const unsigned long long* list = fits ? f.list : keys;
+  const int m = fits ? f.n_list : n;
+  if (fits && tid == 0) f.list[m] = 0ull;
+  __syncthreads();
+  // A key's rank is the number of larger ones: four threads count for a key, or
+  // two or one where there are many; two keys a load.
+  float left = -INFINITY;  // the largest listed logit past the M-th
+  const int share = m <= kRowThreads / 4 ? 4 : (m <= kRowThreads / 2 ? 2 : 1);
+  for (int i0 = 0; i0 < m; i0 += kRowThreads / share) {
+    const int i = i0 + tid / share;
+    const unsigned long long k = i < m ? list[i] : ~0ull;
+    int pos = 0;
+    for (int j = 2 * (tid % share); j < m; j += 2 * share) {
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + j);
+      pos += (q.x > k ? 1 : 0) + (q.y > k ? 1 : 0);
+    }
+    if (share > 1) pos += __shfl_xor_sync(0xFFFFFFFFu, pos, 1);
+    if (share > 2) pos += __shfl_xor_sync(0xFFFFFFFFu, pos, 2);
+    if (i < m && tid % share == 0) {
+      const float z = key_logit(k);
+      if (pos < a.M) {
+        a.tokens[static_cast<long long>(row) * a.M + pos] = key_token(k);
+        a.values[static_cast<long long>(row) * a.M + pos] = z;
+        f.ranked[pos] = z;
+        if (pos == a.M - 1) f.last = k;
+      }
+    }
+  }
+  __syncthreads();
+  const unsigned long long last = f.last;  // the M-th key
+  for (int i = tid; i < n; i += kRowThreads)
+    if (keys[i] < last) left = fmaxf(left, key_logit(keys[i]));
+  left = warp_max_nan(left);
+  if (lane == 0) f.fred[warp] = left;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRowWarps; ++w) ref = fmaxf(ref, f.fred[w]);
+  if (!(ref > -INFINITY)) ref = 0.f;
+  unsigned long long rest = 0ull;  // in 2^-40 of the largest possible term
+  for (int i = tid; i < n; i += kRowThreads)
+    if (keys[i] < last) rest += static_cast<unsigned long long>(ex2((key_logit(keys[i]) - ref) * c) * 1099511627776.f);
+  float top_sum = 0.f;
+  for (int i = tid; i < a.M; i += kRowThreads) top_sum += ex2((f.ranked[i] - row_max) * c);
+  top_sum = warp_sum(top_sum);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xFFFFFFFFu, rest, o);
+  if (lane == 0) {
+    f.dred[warp] = static_cast<double>(top_sum);
+    f.ured[warp] = rest;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  double top_d = 0.0;
+  rest = 0ull;
+#pragma unroll
+  for (int w = 0; w < kRowWarps; ++w) {
+    top_d += f.dred[w];
+    rest += f.ured[w];
+  }
+  double others = 0.0;
+  if (lane < S && f.slices[lane].sum > 0.0)
+    others = f.slices[lane].sum * static_cast<double>(ex2((f.slices[lane].ref - ref) * c));
+  top_logs(a, row, row_max, top_d, ref, warp_sum_d(others) + static_cast<double>(rest) * 9.094947017729282e-13);
+}
+
 template <typename TIn>
 __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
   __shared__ uint64_t bar;
-  __shared__ uint32_t all_maxima[kMaxima];     // written by the cluster's CTAs
-  __shared__ unsigned long long pool[kPool];   // the CTA's candidates; rank 0: then the cluster's
-  __shared__ TopPart parts[kMaxRowCluster];    // written by the cluster's CTAs
-  __shared__ float far_max[kMaxRowCluster];    // likewise
+  __shared__ uint32_t maxima[kMaxima];
+  __shared__ __align__(16) unsigned long long pool[kPool + 2];  // candidates
   __shared__ double dred[kRowWarps];
   __shared__ int ired[kRowWarps];
-  __shared__ int counts[3];                    // per-CTA counts exchanged by the exact select
-  __shared__ int n_mine;                       // this CTA's candidates
+  TopFinish& fin = *reinterpret_cast<TopFinish*>(data);  // over the staged slice, when that is done with
+  __shared__ int n_pool, n_vecs;
   __shared__ uint2 tau_top;
 
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
-  const int row = static_cast<int>(blockIdx.x) / C;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled
+  const int row = static_cast<int>(blockIdx.x) / a.n_slices, part = static_cast<int>(blockIdx.x) - row * a.n_slices;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TIn* src = static_cast<const TIn*>(a.in.base) +
                    row_offset(a.in.batch_stride, a.in.row_stride, a.in.rows_per_batch, row);
-  const Slice s = slice_of(src, a.V, a.slice_vecs, rank);
+  const Slice s = slice_of(src, a.V, a.slice_vecs, part);
   const int base = s.first * VE - s.head;  // token id of the first staged place
-  const double invT = a.inv_t;
+  const int v0 = max(base, 0), v1 = s.count > 0 ? min(base + s.count * VE, a.V) : v0;  // the slice's tokens
   const float c = a.log2e_t;
 
   if (warp == kRowWarps - 1) {
@@ -721,57 +901,30 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
     }
     slice_load(src, a.V, s, data, &bar);
   }
-  if (tid == 0) n_mine = 0;
+  if (tid == 0) n_pool = n_vecs = 0;
+  int timeout = slice_wait(&bar, 0);
+  const TopVecs mine = slice_top_vecs<TIn>(data, s.count);
+  const bool both = a.M > kMaxima / 4;  // with half of the maxima at or above the threshold, 1.4 M candidates
+  // a NaN in the third is the slice's NaN whichever maxima count
+  maxima[tid] = ord_key(mine.third == mine.third ? mine.first : mine.third);
+  if (both) maxima[kRowThreads + tid] = ord_key(mine.second);
   __syncthreads();
-  const bool here = slice_wait(&bar, 0) == 0;
-  const TwoMax mine = slice_two_max<TIn>(data, s.count);
-  const uint32_t my_key = here ? ord_key(fmax_nan(mine.first, mine.second)) : kKeyTimeout;
-  // Groups of threads small enough for twice as many maxima as logits asked
-  // for: with half of the groups at or above the threshold, 1.4 M candidates.
-  const int cluster_up = C <= 1 ? 1 : (C <= 2 ? 2 : (C <= 4 ? 4 : 8));
-  const int per = min((a.M <= kMaxima / 4 ? kMaxima / 2 : kMaxima) / cluster_up, kRowThreads);
-  {
-    uint32_t k = my_key;
-    for (int o = 1; o < kRowThreads / per; o <<= 1) k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, o));
-    const int group = kRowThreads / per;
-    if (tid % group == 0)
-      for (int r = 0; r < C; ++r) cluster.map_shared_rank(&all_maxima[0], r)[rank * per + tid / group] = k;
-  }
-  cluster.sync();
-
-  // The threshold tau: a cut to 16 bits is the M-th maximum or below it.
   if (warp == 0) {
-    const uint2 t = a.M <= kMaxima / 4 ? threshold_and_top<kMaxima / 64>(all_maxima, per * C, a.M)
-                                       : threshold_and_top<kMaxima / 32>(all_maxima, per * C, a.M);
+    const uint2 t = both ? threshold_and_top<kMaxima / 32>(maxima, a.M) : threshold_and_top<kMaxima / 64>(maxima, a.M);
     if (lane == 0) tau_top = t;
   }
   __syncthreads();
-  const uint32_t row_key = tau_top.y;
-  const auto void_row = [&](int status) {
-    if (rank != 0) return;
-    for (int i = tid; i < a.M; i += kRowThreads) {
-      a.tokens[static_cast<long long>(row) * a.M + i] = -1;
-      a.values[static_cast<long long>(row) * a.M + i] = __int_as_float(0x7FC00000);
-    }
-    if (tid == 0) {
-      a.lse[row] = a.tail[row] = __int_as_float(0x7FC00000);
-      a.status[row] = status;
-    }
-  };
-  if (row_key >= ord_key(INFINITY) || row_key <= ord_key(-INFINITY)) {  // the same in every CTA
-    void_row(row_key == kKeyTimeout ? SSD_ROW_DEVICE_TIMEOUT : SSD_ROW_NONFINITE);
-    return;
-  }
-  const float row_max = key_to_float(row_key);
+  const uint32_t top_key = tau_top.y;
+  const bool ranked = top_key < ord_key(INFINITY) && !timeout;  // no NaN, no +inf
   // With fewer maxima than M, or M of them -inf, every logit is a candidate.
   const float tau = tau_top.x <= ord_key(-INFINITY) ? -INFINITY : key_to_float(full_key<TIn>(tau_top.x));
   float ref = tau > -INFINITY ? tau : 0.f;
 
-  // A candidate goes to the CTA's pool, and out of the staged row: what is left
-  // there is the tail.  Past the pool's end nothing is kept, and the row is read
-  // again.
+  // A candidate goes to the pool, and out of the staged slice: what is left
+  // there is the tail.  Past the pool's end nothing is kept, and the slice is
+  // read again.
   const auto take = [&](int i, int e, float z) {
-    const int at = atomicAdd(&n_mine, 1);
+    const int at = atomicAdd(&n_pool, 1);
     if (at < kPool) pool[at] = rank_key(z, base + i * VE + e);
     reinterpret_cast<TIn*>(data + i)[e] = Elem<TIn>::neg_inf();
   };
@@ -779,52 +932,88 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
     const int id = base + i * VE + e;
     return id >= 0 && id < a.V;
   };
-  const auto look = [&](int i) {
-#pragma unroll 1
-    for (int e = 0; e < VE; ++e) {
-      const float z = Elem<TIn>::to_float(reinterpret_cast<const TIn*>(data + i)[e]);
-      if (z >= tau && real(i, e)) take(i, e, z);
+  double below = 0.0;
+  if (ranked && top_key <= ord_key(-INFINITY)) {
+    // nothing but -inf: the first tokens, in order
+    for (int i = tid; i < min(a.M, v1 - v0); i += kRowThreads) pool[i] = rank_key(-INFINITY, v0 + i);
+    if (tid == 0) n_pool = min(a.M, v1 - v0);
+    __syncthreads();
+  } else if (ranked) {
+    // The vectors that hold candidates, gathered first and then looked through
+    // by all threads: done by each thread for its own, this step took half of
+    // the kernel's time.
+    uint16_t* vecs = reinterpret_cast<uint16_t*>(maxima);  // no longer used
+    const auto note = [&](bool on, int i) {
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+      if (who == 0u) return;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&n_vecs, __popc(who));
+      at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
+      if (on && at < kPool) vecs[at] = static_cast<uint16_t>(i);
+    };
+    if (!(tau > -INFINITY)) {  // every vector
+      for (int i0 = tid - lane; i0 < s.count; i0 += kRowThreads) note(i0 + lane < s.count, i0 + lane);
+    } else {
+      note(mine.first >= tau, mine.at);
+      note(mine.second >= tau, mine.at2);
+      if (__any_sync(0xFFFFFFFFu, mine.third >= tau)) {
+        for (int i0 = tid - lane; i0 < s.count; i0 += kRowThreads) {
+          const int i = i0 + lane;
+          note(i < s.count && mine.third >= tau && i != mine.at && i != mine.at2 &&
+                   Elem<TIn>::vec_max(data[i]) >= tau,
+               i);
+        }
+      }
     }
-  };
-  if (s.count > tid) {
-    if (mine.second >= tau) {
-      for (int i = tid; i < s.count; i += kRowThreads)
-        if (Elem<TIn>::vec_max(data[i]) >= tau) look(i);
-    } else if (mine.first >= tau) {
-      look(mine.at);
+    __syncthreads();
+    // A vector per thread: its candidates as a mask, their places by a prefix sum.
+    const int listed = min(n_vecs, kPool);
+    for (int j0 = tid - lane; j0 < listed; j0 += kRowThreads) {
+      const int i = j0 + lane < listed ? vecs[j0 + lane] : 0;
+      uint32_t on = 0u;
+      if (j0 + lane < listed) {
+        float f[VE];
+        Elem<TIn>::unpack(data[i], f);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) on |= f[e] >= tau && real(i, e) ? 1u << e : 0u;
+      }
+      const int k = __popc(on);
+      int inc = k;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      int at = 0;
+      if (lane == 31) at = atomicAdd(&n_pool, inc);
+      at = __shfl_sync(0xFFFFFFFFu, at, 31) + inc - k;
+      for (; on; on &= on - 1u, ++at) {
+        const int e = __ffs(static_cast<int>(on)) - 1;
+        TIn* place = reinterpret_cast<TIn*>(data + i) + e;
+        if (at < kPool) pool[at] = rank_key(Elem<TIn>::to_float(*place), base + i * VE + e);
+        *place = Elem<TIn>::neg_inf();
+      }
     }
+    if (tid == 0 && n_vecs > kPool) n_pool = kPool + 1;
+    __syncthreads();
+    const float sum = slice_exp_sum<TIn>(data, s.count, ref, c);
+    below = block_reduce(static_cast<double>(sum), dred, OpAdd());
   }
-  // Every thread sums its own vectors, so it sees its own candidates gone.
-  const auto publish = [&](float part_sum, int n, int timeout) {
-    const double b = block_reduce(static_cast<double>(part_sum), dred, OpAdd());
-    if (tid < C) cluster.map_shared_rank(&parts[0], tid)[rank] = TopPart{b, n, timeout};
-    cluster.sync();
-  };
-  const float sum = slice_exp_sum<TIn>(data, s.count, ref, c);
-  __syncthreads();  // n_mine
-  publish(sum, n_mine, 0);
-  const auto joined = [&]() {
-    double b = 0.0;
-    for (int r = 0; r < C; ++r) b += parts[r].sum;
-    return b;
-  };
-  double below = joined();
-  int total = 0;
-  for (int r = 0; r < C; ++r) total = min(total + parts[r].count, kPool + 1);
+  int n = n_pool;
 
-  if (total > kPool) {
-    // Exact select, for rows with many equal logits at the threshold: stage the
-    // row again, find the M-th largest key by two bits a pass, then take the
-    // larger ones, and the equal ones in token order.
+  if (n > kPool) {
+    // Exact select, for slices with many equal logits at the threshold: stage
+    // the slice again, find its M-th largest key by two bits a pass, then take
+    // the larger ones, and the equal ones in token order.
     __syncthreads();
     if (warp == kRowWarps - 1) {
       fence_proxy_async_shared();
       slice_load(src, a.V, s, data, &bar);
     }
-    if (tid == 0) n_mine = 0;
-    __syncthreads();
-    const int timeout = slice_wait(&bar, 1);
+    if (tid == 0) n_pool = 0;
+    timeout |= slice_wait(&bar, 1);
     uint32_t prefix = 0u;
+#pragma unroll 1
     for (int bit = 30; bit >= 32 - Elem<TIn>::kKeyBits; bit -= 2) {
       const uint32_t c1 = prefix | (1u << bit), c2 = prefix | (2u << bit), c3 = prefix | (3u << bit);
       int n1 = 0, n2 = 0, n3 = 0;
@@ -842,50 +1031,31 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       n1 = block_reduce(n1, ired, OpAdd());
       n2 = block_reduce(n2, ired, OpAdd());
       n3 = block_reduce(n3, ired, OpAdd());
-      if (tid == 0) counts[0] = n1, counts[1] = n2, counts[2] = n3;
-      cluster.sync();
-      n1 = n2 = n3 = 0;
-      for (int r = 0; r < C; ++r) {
-        const int* q = cluster.map_shared_rank(&counts[0], r);
-        n1 += q[0], n2 += q[1], n3 += q[2];
-      }
-      cluster.sync();  // read before the next pass overwrites them
       prefix = n3 >= a.M ? c3 : (n2 >= a.M ? c2 : (n1 >= a.M ? c1 : prefix));
     }
     const float kth = key_to_float(full_key<TIn>(prefix));
-    int gt = 0, eq = 0;
+    int need = 0;  // of the equal ones, in token order
     for (int i = tid; i < s.count; i += kRowThreads) {
       float f[VE];
       Elem<TIn>::unpack(data[i], f);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        gt += real(i, e) && f[e] > kth;
-        eq += real(i, e) && f[e] == kth;
-      }
+      for (int e = 0; e < VE; ++e) need += real(i, e) && f[e] > kth;
     }
-    gt = block_reduce(gt, ired, OpAdd());
-    eq = block_reduce(eq, ired, OpAdd());
-    if (tid == 0) counts[0] = gt, counts[1] = eq;
-    cluster.sync();
-    int need = a.M, taken = 0;  // of the equal ones, in token order; those in earlier slices
-    for (int r = 0; r < C; ++r) {
-      const int* q = cluster.map_shared_rank(&counts[0], r);
-      need -= q[0];
-      if (r < rank) taken += q[1];
-    }
+    need = a.M - block_reduce(need, ired, OpAdd());
+    int taken = 0;
     for (int i0 = 0; i0 < s.count; i0 += kRowThreads) {
       const int i = i0 + tid;
       float f[VE];
-      int n = 0;
+      int eq = 0;
       if (i < s.count) {
         Elem<TIn>::unpack(data[i], f);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           if (!real(i, e)) f[e] = __int_as_float(0x7FC00000);  // equal to nothing
-          n += f[e] == kth;
+          eq += f[e] == kth;
         }
       }
-      int inc = n;
+      int inc = eq;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -894,7 +1064,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       __syncthreads();
       if (lane == 31) ired[warp] = inc;
       __syncthreads();
-      int before = taken + inc - n, chunk = 0;
+      int before = taken + inc - eq, chunk = 0;
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) {
         if (w < warp) before += ired[w];
@@ -913,83 +1083,57 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       taken += chunk;
     }
     ref = kth > -INFINITY ? kth : 0.f;
-    const float rest = slice_exp_sum<TIn>(data, s.count, ref, c);
-    __syncthreads();  // n_mine
-    publish(rest, n_mine, timeout);
-    below = joined();
-    total = a.M;
-    int late = 0;
-    for (int r = 0; r < C; ++r) late |= parts[r].timeout;
-    if (late) {
-      void_row(SSD_ROW_DEVICE_TIMEOUT);
-      return;
+    below = block_reduce(static_cast<double>(slice_exp_sum<TIn>(data, s.count, ref, c)), dred, OpAdd());
+    n = a.M;
+  }
+  // Others far below the threshold: sum them again around their own maximum.
+  if (ranked && n < v1 - v0 && below < 1e-18) {
+    const float m = static_cast<float>(
+        block_reduce(static_cast<double>(slice_max<TIn>(data, s.count)), dred, OpMax()));
+    if (m > -INFINITY) {
+      ref = m;
+      below = block_reduce(static_cast<double>(slice_exp_sum<TIn>(data, s.count, ref, c)), dred, OpAdd());
     }
   }
 
-  // A tail far below the threshold: sum it again around its own maximum.
-  if (total == a.M && a.V > a.M && below < 1e-18) {
-    const float m = warp_max_nan(slice_max<TIn>(data, s.count));
-    const double tm_cta = block_reduce(static_cast<double>(m), dred, OpMax());
-    if (tid < C) cluster.map_shared_rank(&far_max[0], tid)[rank] = static_cast<float>(tm_cta);
-    cluster.sync();
-    float tm = -INFINITY;
-    for (int r = 0; r < C; ++r) tm = fmaxf(tm, far_max[r]);
-    if (tm > -INFINITY) ref = tm;
-    publish(slice_exp_sum<TIn>(data, s.count, ref, c), n_mine, 0);
-    below = joined();
-  }
-  if (rank != 0) {
-    int off = 0;
-    for (int r = 0; r < rank; ++r) off += parts[r].count;
-    unsigned long long* to = cluster.map_shared_rank(&pool[0], 0);
-    for (int i = tid; i < n_mine && off + i < kPool; i += kRowThreads) to[off + i] = pool[i];
-    cluster.barrier_arrive();  // nothing is written into this CTA any more: it need not wait
+  if (!ranked) n = 0;
+  const uint32_t cut = n >= a.M ? tau_top.x >> 16 : 0u;
+  if (a.n_slices > 1) {
+    const size_t at = static_cast<size_t>(row) * a.n_slices + part;
+    unsigned long long* out = a.keys + at * kPool;
+    __syncthreads();  // the pool
+    for (int i = tid; i < n; i += kRowThreads) out[i] = pool[i];
+    if (tid == 0) a.slices[at] = TopSlice{below, ref, top_key, cut, n, timeout};
     return;
   }
+  if (tid == 0) {
+    fin.slices[0] = TopSlice{below, ref, top_key, cut, n, timeout};
+    pool[n] = 0ull;
+  }
+  top_finish(a, row, pool, n, 1, fin);
+}
 
-  // Order the candidates; those past the M-th belong to the tail. The sums run
-  // over the order, whatever order the candidates came in.
-  float* ranked = reinterpret_cast<float*>(data);
-  int n = 0;
-  for (int r = 0; r < C; ++r) n += parts[r].count;
-  n = min(n, kPool);
-  cluster.sync();  // the others' candidates; the staged logits are no longer read
-  for (int i = tid; i < n; i += kRowThreads) {
-    const unsigned long long k = pool[i];
-    int pos = 0;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) pos += pool[j] > k;
-    const float z = key_to_float(static_cast<uint32_t>(k >> 32));
-    ranked[pos] = z;
-    if (pos < a.M) {
-      a.tokens[static_cast<long long>(row) * a.M + pos] =
-          static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k & 0xFFFFFFFFull));
-      a.values[static_cast<long long>(row) * a.M + pos] = z;
-    }
-  }
+// A CTA per row: the slices' lists, one after the other, then as above.
+__global__ void __launch_bounds__(kRowThreads) ssd_top_join_kernel(const TopArgs a) {
+  extern __shared__ __align__(128) uint4 staged[];
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(staged);  // [n_slices * kPool + 2]
+  __shared__ TopFinish fin;
+  const int row = blockIdx.x, tid = threadIdx.x, S = a.n_slices;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the slices' results
+  if (tid < S) fin.slices[tid] = a.slices[static_cast<size_t>(row) * S + tid];
   __syncthreads();
-  // where every logit was a candidate, the tail's largest is the reference
-  if (!(below > 0.0) && n > a.M) ref = ranked[a.M] > -INFINITY ? ranked[a.M] : 0.f;
-  float top_sum = 0.f, rest = 0.f;
-  for (int i = tid; i < n; i += kRowThreads) {
-    const float z = ranked[i];
-    if (i < a.M)
-      top_sum += ex2((z - row_max) * c);
-    else
-      rest += ex2((z - ref) * c);
+  int n = 0;
+  for (int s = 0; s < S; ++s) n += fin.slices[s].count;
+  for (int s = tid >> 5; s < S; s += kRowWarps) {  // a warp per list
+    const unsigned long long* in = a.keys + (static_cast<size_t>(row) * S + s) * kPool;
+    const int count = fin.slices[s].count;
+    int off = 0;
+    for (int r = 0; r < s; ++r) off += fin.slices[r].count;
+#pragma unroll 4
+    for (int i = tid & 31; i < count; i += 32) keys[off + i] = __ldcg(in + i);
   }
-  const double top_d = block_reduce(static_cast<double>(top_sum), dred, OpAdd());
-  const double rest_d = block_reduce(static_cast<double>(rest), dred, OpAdd());
-  if (warp == 0) {
-    const double t = below + rest_d;  // around ref
-    const double share = t > 0.0 ? t * exp((static_cast<double>(ref) - static_cast<double>(row_max)) * invT) : 0.0;
-    const double logs = log(lane == 0 ? t : top_d + share);  // two logarithms at once
-    if (lane == 0) {
-      a.tail[row] = t > 0.0 ? static_cast<float>(static_cast<double>(ref) * invT + logs) : -INFINITY;
-      a.status[row] = 0;
-    }
-    if (lane == 1) a.lse[row] = static_cast<float>(static_cast<double>(row_max) * invT + logs);
-  }
+  if (tid == 0) keys[n] = 0ull;
+  top_finish(a, row, keys, n, S, fin);
 }
 
 }  // namespace ssd

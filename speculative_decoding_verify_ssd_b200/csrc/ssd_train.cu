@@ -80,6 +80,33 @@ static ssd_status launch_rows(void (*fn)(Args), const Args& a, long long rows, c
   return cudaLaunchKernelEx(&cfg, fn, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
+// The top logits: slices of a row for as many CTAs, each row's own or joined.
+struct TopPlan {
+  int slices, slice_vecs, smem;
+  size_t keys, total;  // workspace: the slices' records, then their sorted keys
+};
+
+static bool top_plan(long long rows, int V, int esize, TopPlan* p) {
+  const long long vecs = (static_cast<long long>(V) * esize + 15) / 16 + 1;  // a row may start inside a vector
+  const long long bytes = vecs * 16;
+  long long n = (bytes + kSliceTarget - 1) / kSliceTarget;
+  const long long fill = (kRowFill + rows - 1) / rows, by_len = bytes / kSliceMin;
+  const long long extra = fill < by_len ? fill : by_len;
+  if (n < extra) n = extra;
+  if (n > kMaxTopSlices) n = kMaxTopSlices;
+  const long long sv = (vecs + n - 1) / n;
+  if (sv * 16 > kSliceMax || rows * n > 0x7FFFFFFFLL) return false;
+  p->slices = static_cast<int>(n);
+  p->slice_vecs = static_cast<int>(sv);
+  p->smem = static_cast<int>(n > 1 || sv * 16 > static_cast<long long>(sizeof(TopFinish)) ? sv * 16 : sizeof(TopFinish));
+  p->keys = p->total = 0;
+  if (n > 1) {
+    p->keys = static_cast<size_t>(rows * n) * sizeof(TopSlice);
+    p->total = p->keys + static_cast<size_t>(rows * n) * kPool * 8;
+  }
+  return true;
+}
+
 // Checks common to the row calls.
 static ssd_status check_rows(int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,
                              int64_t row_stride, float T, int M) {
@@ -325,18 +352,25 @@ using namespace ssd;
 
 extern "C" {
 
+size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M) {
+  TopPlan p;
+  if (check_rows(dtype, 1, rows, V, 0, 0, 1.f, M) != SSD_OK || rows == 0) return 0;
+  return top_plan(rows, V, dtype == SSD_DTYPE_FP32 ? 4 : 2, &p) ? p.total : 0;
+}
+
 ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,
                            int64_t row_stride, float T, int M, int32_t* tokens, float* values, float* lse, float* tail,
-                           int32_t* status, void* stream) {
+                           int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
   const ssd_status st = check_rows(dtype, n_batch, rows_per_batch, V, batch_stride, row_stride, T, M);
   if (st != SSD_OK) return st;
   const long long rows = static_cast<long long>(n_batch) * rows_per_batch;
   if (rows == 0) return SSD_OK;
   if (!logits || !tokens || !values || !lse || !tail || !status) return SSD_ERR_INVALID_ARG;
   const int esize = dtype == SSD_DTYPE_FP32 ? 4 : 2;
-  if (!aligned_to(logits, esize)) return SSD_ERR_ALIGNMENT;
-  RowPlan p;
-  if (!row_plan(rows, V, esize, kTopMinBytes, &p)) return SSD_ERR_UNSUPPORTED;
+  if (!aligned_to(logits, esize) || !aligned_to(workspace, 256)) return SSD_ERR_ALIGNMENT;
+  TopPlan p;
+  if (!top_plan(rows, V, esize, &p)) return SSD_ERR_UNSUPPORTED;
+  if (p.total > 0 && (!workspace || ws_bytes < p.total)) return SSD_ERR_WORKSPACE;
   TopArgs a;
   const bool one = n_batch == 1 || batch_stride == row_stride * rows_per_batch;
   a.in = RowsIn{logits, batch_stride, row_stride, one ? 0 : rows_per_batch};
@@ -345,14 +379,35 @@ ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_
   a.lse = lse;
   a.tail = tail;
   a.status = status;
+  a.slices = static_cast<TopSlice*>(workspace);
+  a.keys = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + p.keys);
   a.V = V;
   a.M = M;
   a.slice_vecs = p.slice_vecs;
+  a.n_slices = p.slices;
   a.inv_t = 1.0 / static_cast<double>(T);
   a.log2e_t = static_cast<float>(1.4426950408889634 * a.inv_t);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == SSD_DTYPE_BF16 ? launch_rows(&ssd_top_kernel<uint16_t>, a, rows, p, s)
-                                 : launch_rows(&ssd_top_kernel<float>, a, rows, p, s);
+  void (*fn)(TopArgs) = dtype == SSD_DTYPE_BF16 ? &ssd_top_kernel<uint16_t> : &ssd_top_kernel<float>;
+  const int join_smem = (p.slices * kPool + 2) * 8;
+  if (allow_smem(reinterpret_cast<const void*>(fn), p.smem) != cudaSuccess ||
+      allow_smem(reinterpret_cast<const void*>(&ssd_top_join_kernel), join_smem) != cudaSuccess)
+    return SSD_ERR_CUDA;
+  fn<<<static_cast<unsigned>(rows * p.slices), kRowThreads, p.smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
+  if (p.slices == 1) return SSD_OK;
+  // a programmatic dependent: scheduled while the last slices run, it waits for them
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(join_smem);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ssd_top_join_kernel, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,

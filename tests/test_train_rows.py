@@ -20,7 +20,7 @@ def _top(L, **kw):
     a = dict(logits=None, dtype=1, nb=2, rpb=3, V=100, bs=300, rs=100, T=1.0, M=4)
     a.update(kw)
     return L.ssd_teacher_top(a["logits"], a["dtype"], a["nb"], a["rpb"], a["V"], a["bs"], a["rs"], a["T"], a["M"],
-                             None, None, None, None, None, None)
+                             None, None, None, None, None, a.get("work"), a.get("n", 0), None)
 
 
 def _distill(L, **kw):
@@ -365,7 +365,11 @@ def test_rows_binding_refusals():
     with pytest.raises(ssd.SsdError):
         ssd.ssd_distill(z, tokens, values, tail, T=0.0)
     with pytest.raises(ssd.SsdError, match="too large"):
-        ssd.ssd_teacher_top(torch.zeros(1, 1 << 20, device="cuda"), 1)
+        ssd.ssd_distill(torch.zeros(1, 1 << 20, device="cuda"), tokens[:1], values[:1])
+    with pytest.raises(ssd.SsdError, match="too large"):
+        ssd.ssd_teacher_top(torch.zeros(1, 1 << 22, device="cuda"), 1)
+    with pytest.raises(ssd.SsdError, match="workspace"):
+        ssd.ssd_teacher_top(logits_like((1,), 70000, BF16, 1), 4, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     e = ssd.ssd_teacher_top(z[:0], 4)
     assert e.tokens.shape == (0, 4) and ssd.ssd_distill(z[:0], tokens[:0], values[:0]).grad.shape == (0, 50)
 
