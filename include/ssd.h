@@ -73,7 +73,7 @@ enum { SSD_FANOUT_GEOMETRIC = 0, SSD_FANOUT_UNIFORM = 1 };
 #define SSD_MAX_TOP 256           /* teacher logits kept per row (ssd_teacher_top, ssd_distill) */
 #define SSD_MIN_TRAIN_T 1e-4f     /* temperatures of ssd_teacher_top and ssd_distill */
 #define SSD_MAX_TRAIN_T 1e4f
-#define SSD_MAX_LINEAR_N (1 << 20) /* rows, width and vocabulary of ssd_linear_ce */
+#define SSD_MAX_LINEAR_N (1 << 18) /* rows, width and vocabulary of ssd_linear_ce */
 #define SSD_MAX_LINEAR_D (1 << 16)
 #define SSD_MAX_LINEAR_V (1 << 24)
 
@@ -395,8 +395,8 @@ size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
  * With ssd_teacher_top's tokens, values and tail at the same T this is the
  * divergence between target and draft with the target's tail as one event;
  * with tail NULL (or -inf) the top is renormalised and q stays whole.
- *   tokens [rows, M]: distinct ids, -1 for an absent atom; values [rows, M]
- *   (-inf: no weight); tail [rows] or NULL.  row_scale [rows] or NULL (1): the
+ *   1 <= M <= min(V, SSD_MAX_TOP).  tokens [rows, M]: distinct ids, in any
+ *   order, -1 for an absent atom; values [rows, M] (-inf: no weight); tail [rows] or NULL.  row_scale [rows] or NULL (1): the
  *   factor of the row's gradient (loss is not scaled).  A row of row_scale 0
  *   is left out: its logits and teacher are not read, loss 0, gradient 0.
  *   loss [rows], status [rows] out.  grad: NULL, or the gradient with respect

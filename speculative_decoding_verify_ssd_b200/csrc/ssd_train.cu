@@ -20,7 +20,8 @@ static std::mutex g_fn_mu;
 static std::map<std::pair<const void*, int>, int> g_fn_smem;
 
 // Raises a kernel's dynamic shared-memory limit on the current device, once.
-static cudaError_t allow_smem(const void* fn, int bytes) {
+// Nothing is thrown past the C entry points.
+static cudaError_t allow_smem(const void* fn, int bytes) try {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -30,6 +31,8 @@ static cudaError_t allow_smem(const void* fn, int bytes) {
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) have = bytes;
   return e;
+} catch (...) {
+  return cudaErrorMemoryAllocation;
 }
 
 // ---------------------------------------------------------------------------

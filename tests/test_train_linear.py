@@ -111,9 +111,24 @@ def test_larger(N, D, V):
 
 
 @pytest.mark.gpu
+def test_scales():
+    """Signs, magnitudes far apart, and one scale for all: what is largest sets the common factor."""
+    hidden, weight, targets = linear_case((150,), 72, 400, 19)
+    g = torch.Generator(device="cuda").manual_seed(20)
+    check(hidden, weight, targets, torch.randn(150, generator=g, device="cuda"))
+    check(hidden, weight, targets, -torch.rand(150, generator=g, device="cuda") * 1e-6)
+    check(hidden, weight, targets, 10.0 ** torch.randint(-12, 5, (150,), generator=g, device="cuda").float())
+    same = torch.full((150,), 1.0 / 37, device="cuda")
+    r = ssd.ssd_linear_ce(hidden, weight, targets)
+    one, scaled = (ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse, row_scale=s) for s in (None, same))
+    for a, b in zip(one, scaled):    # the same sums, times 1/37, rounded: a bf16 step of each at most
+        assert ((a.double() / 37 - b.double()).abs() <= 2.0 ** -7 * b.double().abs() + 1e-38).all()
+
+
+@pytest.mark.gpu
 def test_pieces():
     """More rows than one piece of the vocabulary holds the logits of."""
-    N, D, V = 5000, 64, 30001
+    N, D, V = 5000, 64, 60001
     hidden, weight, targets = linear_case((N,), D, V, 3, keep=0.8)
     check(hidden, weight, targets, torch.rand(N, device="cuda") / N)
 

@@ -2,6 +2,10 @@
 verified, the target's top logits kept, the draft's logits distilled on them
 and its head trained on the verified tokens; the gradients against automatic
 differentiation in 64 bits."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -102,3 +106,37 @@ def test_step_captured():
     for a, b in ((r.out_tokens, r2.out_tokens), (top.tokens, top2.tokens), (top.tail, top2.tail),
                  (dis.loss, dis2.loss), (dis.grad, dis2.grad), (y, y2), (ce.loss, ce2.loss), (dh, dh2), (dw, dw2)):
         assert torch.equal(a, b)
+
+
+FIRST = """
+import sys, torch
+sys.path[:0] = [%r, %r]
+import test_train_together as t
+from speculative_decoding_verify_ssd_b200 import binding as ssd
+x = t.inputs(400)
+draft = (x["hidden"].reshape(-1, t.D) @ x["weight"].t()).view(t.B, t.K, t.V)
+y = x["drafts"]
+torch.cuda.synchronize()
+def calls():
+    top = ssd.ssd_teacher_top(x["target"][:, :t.K], t.M)
+    dis = ssd.ssd_distill(draft, top.tokens, top.values, top.tail, row_scale=x["scale"])
+    ce = ssd.ssd_linear_ce(x["hidden"], x["weight"], y)
+    return (top.tokens, dis.loss, dis.grad, ce.loss) + ssd.ssd_linear_ce_grad(x["hidden"], x["weight"], y, ce.lse)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+torch.cuda.synchronize()
+for a, b in zip(out, calls()):
+    assert torch.equal(a, b)
+print("first calls captured")
+"""
+
+
+@pytest.mark.gpu
+def test_first_calls_in_a_capture():
+    """A process whose first training calls are captured."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST % (here, os.path.dirname(here))], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "first calls captured" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
