@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const GemmWait<CG> wait = {&abort_flag, a.error};
+  stream_wait();
   const int n_active = a.hdr->n_active;
   const float scale_max = a.hdr->scale_max;
   const GemmWork<Op, CG> work(a, n_active);
@@ -592,6 +593,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
   __shared__ int place[32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n0 = static_cast<int>(blockIdx.x) * a.block_rows;
+  stream_wait();
   // Every block counts the rows itself: one launch, and 4 bytes a row from L2.
   int before = 0, total = 0;
   float top = 0.f;
@@ -687,6 +689,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ double sums[32][kJoinRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = tid % kJoinRows;
   const int row0 = static_cast<int>(blockIdx.x) * kJoinRows, row = row0 + r;
+  stream_wait();
   const int n_active = hdr->n_active;
   if (row0 >= n_active) return;
   const bool live = row < n_active;
@@ -749,6 +752,7 @@ __global__ void __launch_bounds__(kDhThreads)
                          uint16_t* grad_hidden, int32_t* status) {
   const int r = static_cast<int>(blockIdx.x);
   const int d = (static_cast<int>(blockIdx.y) * kDhThreads + static_cast<int>(threadIdx.x)) * 4;
+  stream_wait();
   const LinearHdr h = *hdr;
   if (r >= h.n_active || d >= D) return;
   const int n = index[r];

@@ -23,6 +23,15 @@ constexpr int kMaxRowCluster = 8;   // the portable cluster size
 constexpr int kPool = 448;          // top candidates ranked at once (even)
 constexpr unsigned long long kRowWaitNs = 1000000000ull;  // limit of the wait for a slice's bytes
 
+// The training kernels are launched as programmatic dependents: a kernel's
+// blocks may be scheduled while the kernel before it in the stream still runs,
+// and wait here until that one has completed, before they touch global memory.
+// Behind the wait the next kernel may be scheduled in the same way.
+__device__ __forceinline__ void stream_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Rows of a [n_batch, rows_per_batch, V] tensor, strides in elements.
 struct RowsIn {
   const void* base;
@@ -379,6 +388,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
   TIn* dst = a.grad ? static_cast<TIn*>(a.grad) +
                           row_offset(a.g_batch_stride, a.g_row_stride, a.in.rows_per_batch, row)
                     : nullptr;
+  stream_wait();
   // All of the row's small inputs are asked for at once; one atom per thread.
   const float scale = a.row_scale ? a.row_scale[row] : 1.f;
   const float tail_in = a.tail ? a.tail[row] : -INFINITY;
@@ -884,7 +894,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
   __shared__ int n_pool, n_vecs;
   __shared__ uint2 tau_top;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled
+  stream_wait();
   const int row = static_cast<int>(blockIdx.x) / a.n_slices, part = static_cast<int>(blockIdx.x) - row * a.n_slices;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TIn* src = static_cast<const TIn*>(a.in.base) +
@@ -1119,7 +1129,7 @@ __global__ void __launch_bounds__(kRowThreads) ssd_top_join_kernel(const TopArgs
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(staged);  // [n_slices * kPool + 2]
   __shared__ TopFinish fin;
   const int row = blockIdx.x, tid = threadIdx.x, S = a.n_slices;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the slices' results
+  stream_wait();  // the slices' results
   if (tid < S) fin.slices[tid] = a.slices[static_cast<size_t>(row) * S + tid];
   __syncthreads();
   int n = 0;

@@ -35,6 +35,29 @@ static cudaError_t allow_smem(const void* fn, int bytes) try {
   return cudaErrorMemoryAllocation;
 }
 
+// Launches a kernel as a programmatic dependent of the one before it in the
+// stream (it waits for that one itself), in clusters of `cluster` blocks.
+template <typename... P, typename... A>
+static ssd_status launch_dependent(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
+                                   const A&... args) {
+  if (smem > 0 && allow_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return SSD_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------------------
 // Rows in cluster shared memory.
 // ---------------------------------------------------------------------------
@@ -63,24 +86,6 @@ static bool row_plan(long long rows, int V, int esize, int min_bytes, RowPlan* p
   p->slice_vecs = static_cast<int>(sv);
   p->smem = static_cast<int>(sv * 16 > min_bytes ? sv * 16 : min_bytes);
   return true;
-}
-
-template <typename Args>
-static ssd_status launch_rows(void (*fn)(Args), const Args& a, long long rows, const RowPlan& p, cudaStream_t stream) {
-  if (allow_smem(reinterpret_cast<const void*>(fn), p.smem) != cudaSuccess) return SSD_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * p.cluster));
-  cfg.blockDim = dim3(kRowThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 // The top logits: slices of a row for as many CTAs, each row's own or joined.
@@ -220,23 +225,10 @@ static LinearPlan linear_plan(int N, int D, int V, bool grad) {
 template <int Op, int CG>
 static ssd_status launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a,
                               long long most_tiles, cudaStream_t stream) {
-  const auto fn = &ssd_gemm_kernel<Op, CG>;
-  if (allow_smem(reinterpret_cast<const void*>(fn), GemmShape<Op, CG>::kSmem) != cudaSuccess) return SSD_ERR_CUDA;
   const long long fit = kSmCount / CG;
   const long long groups = most_tiles < fit ? most_tiles : fit;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * CG));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = GemmShape<Op, CG>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, ma, mb, mo, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  return launch_dependent(&ssd_gemm_kernel<Op, CG>, dim3(static_cast<unsigned>(groups * CG)), kGemmThreads,
+                          GemmShape<Op, CG>::kSmem, CG, stream, ma, mb, mo, a);
 }
 
 static ssd_status check_linear(int dtype, int n_batch, int rows_per_batch, int D, int V, int64_t batch_stride,
@@ -273,8 +265,8 @@ static ssd_status launch_prep(PrepArgs& a, cudaStream_t stream) {
   a.block_rows = rows;
   const int blocks = (a.N + rows - 1) / rows;
   const int zero = a.grad_hidden ? kBlockK / kRowWarps : 1;  // blocks that clear the rows behind the last
-  ssd_linear_prep_kernel<<<blocks < zero ? zero : blocks, kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  return launch_dependent(&ssd_linear_prep_kernel, dim3(static_cast<unsigned>(blocks < zero ? zero : blocks)),
+                          kRowThreads, 0, 0, stream, a);
 }
 
 static GemmArgs gemm_args(const LinearPlan& p, char* ws, int V, int D) {
@@ -302,9 +294,10 @@ static ssd_status linear_forward(const LinearPlan& p, char* ws, const void* weig
   const long long most = static_cast<long long>(p.rows / GemmShape<kOpLse, CG>::kTileM) * p.tiles;
   const ssd_status st = launch_gemm<kOpLse, CG>(mh, mw, mw, g, most, stream);
   if (st != SSD_OK) return st;
-  ssd_linear_join_kernel<<<(N + kJoinRows - 1) / kJoinRows, kJoinThreads, 0, stream>>>(
-      g.hdr, g.part, p.rows, p.tiles, reinterpret_cast<const int32_t*>(ws + p.index), g.zt, loss, lse, status);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  return launch_dependent(&ssd_linear_join_kernel, dim3(static_cast<unsigned>((N + kJoinRows - 1) / kJoinRows)),
+                          kJoinThreads, 0, 0, stream, g.hdr, static_cast<const float2*>(g.part), p.rows, p.tiles,
+                          reinterpret_cast<const int32_t*>(ws + p.index), static_cast<const float*>(g.zt), loss, lse,
+                          status);
 }
 
 template <int CG>
@@ -343,10 +336,9 @@ static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* wei
     if (st != SSD_OK) return st;
   }
   const dim3 grid(static_cast<unsigned>(N), static_cast<unsigned>((D / 4 + kDhThreads - 1) / kDhThreads));
-  ssd_linear_dh_kernel<<<grid, kDhThreads, 0, stream>>>(g.hdr, reinterpret_cast<const float*>(ws + p.dh), p.rows,
-                                                        p.slots, D, reinterpret_cast<const int32_t*>(ws + p.index),
-                                                        static_cast<uint16_t*>(grad_hidden), status);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  return launch_dependent(&ssd_linear_dh_kernel, grid, kDhThreads, 0, 0, stream, g.hdr,
+                          reinterpret_cast<const float*>(ws + p.dh), p.rows, p.slots, D,
+                          reinterpret_cast<const int32_t*>(ws + p.index), static_cast<uint16_t*>(grad_hidden), status);
 }
 
 }  // namespace ssd
@@ -392,25 +384,11 @@ ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_
   a.log2e_t = static_cast<float>(1.4426950408889634 * a.inv_t);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   void (*fn)(TopArgs) = dtype == SSD_DTYPE_BF16 ? &ssd_top_kernel<uint16_t> : &ssd_top_kernel<float>;
-  const int join_smem = (p.slices * kPool + 2) * 8;
-  if (allow_smem(reinterpret_cast<const void*>(fn), p.smem) != cudaSuccess ||
-      allow_smem(reinterpret_cast<const void*>(&ssd_top_join_kernel), join_smem) != cudaSuccess)
-    return SSD_ERR_CUDA;
-  fn<<<static_cast<unsigned>(rows * p.slices), kRowThreads, p.smem, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
-  if (p.slices == 1) return SSD_OK;
-  // a programmatic dependent: scheduled while the last slices run, it waits for them
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(kRowThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(join_smem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ssd_top_join_kernel, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  const ssd_status done =
+      launch_dependent(fn, dim3(static_cast<unsigned>(rows * p.slices)), kRowThreads, p.smem, 0, s, a);
+  if (done != SSD_OK || p.slices == 1) return done;
+  return launch_dependent(&ssd_top_join_kernel, dim3(static_cast<unsigned>(rows)), kRowThreads,
+                          (p.slices * kPool + 2) * 8, 0, s, a);
 }
 
 ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,
@@ -449,8 +427,8 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
   a.inv_t = 1.0 / static_cast<double>(T);
   a.log2e_t = static_cast<float>(1.4426950408889634 * a.inv_t);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dtype == SSD_DTYPE_BF16 ? launch_rows(&ssd_distill_kernel<uint16_t>, a, rows, p, s)
-                                 : launch_rows(&ssd_distill_kernel<float>, a, rows, p, s);
+  void (*fn)(DistillArgs) = dtype == SSD_DTYPE_BF16 ? &ssd_distill_kernel<uint16_t> : &ssd_distill_kernel<float>;
+  return launch_dependent(fn, dim3(static_cast<unsigned>(rows * p.cluster)), kRowThreads, p.smem, p.cluster, s, a);
 }
 
 size_t ssd_linear_ce_workspace_bytes(int N, int D, int V, int grad) {
