@@ -369,7 +369,7 @@ def test_rows_binding_refusals():
     with pytest.raises(ssd.SsdError, match="too large"):
         ssd.ssd_teacher_top(torch.zeros(1, 1 << 22, device="cuda"), 1)
     with pytest.raises(ssd.SsdError, match="workspace"):
-        ssd.ssd_teacher_top(logits_like((1,), 70000, BF16, 1), 4, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        ssd.ssd_teacher_top(logits_like((1,), 200001, BF16, 1), 4, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     e = ssd.ssd_teacher_top(z[:0], 4)
     assert e.tokens.shape == (0, 4) and ssd.ssd_distill(z[:0], tokens[:0], values[:0]).grad.shape == (0, 50)
 
