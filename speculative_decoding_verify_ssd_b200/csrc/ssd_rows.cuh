@@ -852,11 +852,15 @@ __device__ __forceinline__ void top_finish(const TopArgs& a, int row, unsigned l
   if (lane == 0) f.fred[warp] = left;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) ref = fmaxf(ref, f.fred[w]);
+  for (int w = 0; w < kRowWarps; ++w) left = fmaxf(left, f.fred[w]);
+  ref = fmaxf(ref, left);
   if (!(ref > -INFINITY)) ref = 0.f;
-  unsigned long long rest = 0ull;  // in 2^-40 of the largest possible term
+  if (!(left > -INFINITY)) left = 0.f;
+  // The listed others in 2^-40 of their own largest: a slice's reference can lie
+  // far above them.
+  unsigned long long rest = 0ull;
   for (int i = tid; i < n; i += kRowThreads)
-    if (keys[i] < last) rest += static_cast<unsigned long long>(ex2((key_logit(keys[i]) - ref) * c) * 1099511627776.f);
+    if (keys[i] < last) rest += static_cast<unsigned long long>(ex2((key_logit(keys[i]) - left) * c) * 1099511627776.f);
   float top_sum = 0.f;
   for (int i = tid; i < a.M; i += kRowThreads) top_sum += ex2((f.ranked[i] - row_max) * c);
   top_sum = warp_sum(top_sum);
@@ -878,7 +882,8 @@ __device__ __forceinline__ void top_finish(const TopArgs& a, int row, unsigned l
   double others = 0.0;
   if (lane < S && f.slices[lane].sum > 0.0)
     others = f.slices[lane].sum * static_cast<double>(ex2((f.slices[lane].ref - ref) * c));
-  top_logs(a, row, row_max, top_d, ref, warp_sum_d(others) + static_cast<double>(rest) * 9.094947017729282e-13);
+  const double rest_d = static_cast<double>(rest) * 9.094947017729282e-13 * static_cast<double>(ex2((left - ref) * c));
+  top_logs(a, row, row_max, top_d, ref, warp_sum_d(others) + (rest > 0ull ? rest_d : 0.0));
 }
 
 template <typename TIn>

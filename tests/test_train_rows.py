@@ -102,6 +102,7 @@ def test_top_sizes(dtype, V, M):
 def test_top_many_rows():
     check_top(logits_like((100, 8), 4001, BF16, 5), 16, 1.0)
     check_top(logits_like((1500,), 1000, FP32, 6), 8, 1.3)
+    check_top(logits_like((50, 6), 70001, BF16, 7), 100, 0.8)    # several slices each
 
 
 @pytest.mark.gpu
@@ -116,6 +117,7 @@ def test_top_views(dtype):
     check_top(x[:, :, 3:4000], 17, 1.0)
     check_top(x[1, 2, 5:], 3, 1.0)
     check_top(x[:1].expand(4, 5, 4099), 9, 1.0)
+    check_top(logits_like((2, 4), 210003, dtype, 2)[:, 1:], 17, 1.0)
 
 
 @pytest.mark.gpu
@@ -141,10 +143,10 @@ def test_top_ties(dtype, V):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("T", [1.0, 0.01, 100.0])
-def test_top_tail_far_below(dtype, T):
+@pytest.mark.parametrize("V", [9001, 240007])
+def test_top_tail_far_below(dtype, T, V):
     """The tail's logarithm stays exact when the top outweighs it by more than
     the exponent range of fp32, with and without ties at the threshold."""
-    V = 9001
     x = logits_like((3,), V, FP32, 11).clamp(-8, 8)
     x[:, [3, 500, 9000]] += 4000.0
     check_top(x.to(dtype), 3, T)
