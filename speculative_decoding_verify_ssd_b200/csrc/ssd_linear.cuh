@@ -1,17 +1,19 @@
 // ssd_linear.cuh -- the cross entropy of a linear head and its gradients
 // without stored logits (ssd_linear_ce, ssd_linear_ce_grad): one persistent
-// tcgen05 matrix-product kernel in four forms that differ in which operands
+// tcgen05 matrix-product kernel in forms that differ in which operands
 // they read and in what their epilogue does with a tile.
 //
 //   lse   z = H W^T            -> per row and vocabulary tile: max, sum exp(z - max); the target's logit
 //   grad  G = s (softmax(z) - onehot)  in bf16, one piece of the vocabulary at a time
-//   dh    dH += G W            -> fp32, one slot per split of the piece
-//   dw    dW = G^T H           -> bf16
+//   back  dH += G W            -> fp32, one slot per split of the piece
+//         dW = G^T H           -> bf16; the tiles of both in one launch, or of one of them
 #pragma once
 
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "../../include/ssd.h"
 #include "ssd_device.cuh"
@@ -26,18 +28,20 @@ constexpr int kATile = 128 * kBlockK * 2;
 constexpr int kOutBuf = 32 * 128;  // one epilogue warp's staging buffer: 32 rows of 128 bytes
 constexpr unsigned long long kGemmWaitNs = 2000000000ull;
 
-enum GemmOp { kOpLse = 0, kOpGrad = 1, kOpDh = 2, kOpDw = 3 };
+enum GemmOp { kOpLse = 0, kOpGrad = 1, kOpBack = 2, kOpDh = 3, kOpDw = 4 };
+constexpr bool is_back(int op) { return op >= kOpBack; }
 
 // A pair of CTAs (CG = 2) computes 256 x 256 tiles, each CTA staging half of
 // either operand.  A single CTA, for up to 128 rows, where the weight's bytes
 // bound the call, computes tiles of 128 x 128: narrow ones leave less of the
 // last wave idle (64 rows over 128256: 7 waves of 128 columns against 4 of
-// 256).  Its dw tiles, bound by what they write, are 128 x 256: 102 us against
-// 117 there.
+// 256).  Its tiles of the back form are 128 x 256: dW, bound by what it writes,
+// took 102 us in them against 117 in 128 x 128; dH alone, bound by the weights it
+// reads, 82 us in narrow ones against 95.
 template <int Op, int CG>
 struct GemmShape {
   static constexpr int kTileM = 128 * CG;
-  static constexpr int kTileN = Op == kOpDw ? 256 : 128 * CG;
+  static constexpr int kTileN = Op == kOpBack || Op == kOpDw ? 256 : 128 * CG;
   static constexpr int kBRows = kTileN / CG;  // the CTA's share of the B tile
   static constexpr int kBTile = kBRows * kBlockK * 2;
   static constexpr int kStage = kATile + kBTile;
@@ -62,7 +66,7 @@ struct GemmArgs {
   int rows;         // padded row count: leading dimension of part, rows of one dh slot
   int V, D;
   int v0, v_count;  // the piece of the vocabulary
-  int slots, first; // dh: splits of the piece; whether it is the first piece
+  int slots, first; // back: splits of the piece; whether it is the first piece
 };
 
 // ---------------------------------------------------------------------------
@@ -216,50 +220,85 @@ struct GemmWait {
 // One tile of a form's work list.
 struct GemmTile {
   int m, n, slot, kb0, kb1;
+  bool dw;  // back: of dW, else of dH
 };
 
+// The tiles of one group (a CTA, or a pair of them), `count` of them.  lse and
+// grad: every step-th tile.  back: every step-th tile of dH, then dW's.  Groups
+// that have one dH tile less take `ratio` dW tiles (that tile's cost) among
+// themselves before all groups take them in turn, so neighbours in time share
+// what they read.
 template <int Op, int CG>
 struct GemmWork {
-  int m_tiles, n_tiles, k_blocks, count;
-  __device__ __forceinline__ GemmWork(const GemmArgs& a, int n_active) {
+  int m_tiles, n_tiles, k_blocks, all;   // dH's in the back form
+  int n_dw, k_dw, more, ratio, n_dh;
+  int group, step, count;
+  __device__ __forceinline__ GemmWork(const GemmArgs& a, int n_active, int g, int groups) {
     const int na = max(n_active, 1);
     constexpr int TM = GemmShape<Op, CG>::kTileM, TN = GemmShape<Op, CG>::kTileN;
-    if (Op == kOpDw) {
-      m_tiles = (a.v_count + TM - 1) / TM;
-      n_tiles = (a.D + TN - 1) / TN;
-      k_blocks = (na + kBlockK - 1) / kBlockK;
-    } else {
-      m_tiles = (na + TM - 1) / TM;
-      n_tiles = ((Op == kOpDh ? a.D : a.v_count) + TN - 1) / TN;
-      k_blocks = ((Op == kOpDh ? a.v_count : a.D) + kBlockK - 1) / kBlockK;
+    group = g;
+    step = groups;
+    m_tiles = (na + TM - 1) / TM;
+    n_tiles = ((is_back(Op) ? a.D : a.v_count) + TN - 1) / TN;
+    k_blocks = ((is_back(Op) ? a.v_count : a.D) + kBlockK - 1) / kBlockK;
+    all = !is_back(Op) ? m_tiles * n_tiles : Op != kOpDw ? m_tiles * n_tiles * a.slots : 0;
+    count = n_dh = g < all ? (all - g + groups - 1) / groups : 0;
+    if (is_back(Op)) {
+      n_dw = n_tiles;
+      k_dw = (na + kBlockK - 1) / kBlockK;
+      const int total = Op != kOpDh ? (a.v_count + TM - 1) / TM * n_dw : 0;
+      more = all % groups;  // the groups below have one dH tile more
+      const int cost = dw_cost(k_dw), few = groups - more;
+      ratio = Op == kOpBack ? min((k_blocks / a.slots + cost / 2) / cost, (total + few - 1) / few) : 0;
+      const int own = total - ratio * few;  // tiles of the common turns; may be negative by less than `few`
+      if (own >= 0)
+        count += (g < more ? 0 : ratio) + (g < own ? (own - g + groups - 1) / groups : 0);
+      else
+        count += g < more ? 0 : ratio - (g - more >= few + own ? 1 : 0);
     }
-    count = m_tiles * n_tiles * (Op == kOpDh ? a.slots : 1);
+  }
+  // A dW tile's time in blocks of k: at least its epilogue's.
+  static __host__ __device__ __forceinline__ int dw_cost(int k_dw) {
+    const int least = CG == 1 ? 2 : 8;
+    return k_dw > least ? k_dw : least;
   }
   // Neighbouring tiles share the operand that is dear: the weight tile (lse,
-  // grad, dh), or the piece's columns (dw).
-  __device__ __forceinline__ GemmTile at(const GemmArgs& a, int t) const {
+  // grad, dH), or the piece's columns (dW).
+  __device__ __forceinline__ GemmTile at(const GemmArgs& a, int i) const {
     GemmTile r;
     r.slot = 0;
-    if (Op == kOpDw) {
-      r.n = t % n_tiles;
-      r.m = t / n_tiles;
-    } else {
-      if (Op == kOpDh) {
-        r.slot = t / (m_tiles * n_tiles);
-        t -= r.slot * m_tiles * n_tiles;
-      }
-      if (Op == kOpGrad) t = count - 1 - t;  // the forward call went upwards: its last weights may be in L2
-      r.m = t % m_tiles;
-      r.n = t / m_tiles;
-    }
     r.kb0 = 0;
+    r.dw = Op == kOpDw;
+    if (is_back(Op) && i >= n_dh) {
+      i -= n_dh;
+      const int first = group < more ? 0 : ratio, few = step - more;
+      const int t = i < first ? i * few + group - more : ratio * few + (i - first) * step + group;
+      r.dw = true;
+      r.n = t % n_dw;
+      r.m = t / n_dw;
+      r.kb1 = k_dw;
+      return r;
+    }
+    int t = group + i * step;
+    if (is_back(Op)) {
+      r.slot = t / (m_tiles * n_tiles);
+      t -= r.slot * m_tiles * n_tiles;
+    }
+    if (Op == kOpGrad) t = all - 1 - t;  // the forward call went upwards: its last weights may be in L2
+    r.m = t % m_tiles;
+    r.n = t / m_tiles;
     r.kb1 = k_blocks;
-    if (Op == kOpDh) {
+    if (is_back(Op)) {
       r.kb0 = static_cast<int>(static_cast<long long>(k_blocks) * r.slot / a.slots);
       r.kb1 = static_cast<int>(static_cast<long long>(k_blocks) * (r.slot + 1) / a.slots);
     }
     return r;
   }
+};
+
+// The tensor maps of a launch; the second set is dW's in the back form.
+struct GemmMaps {
+  CUtensorMap a, b, out, a2, b2, out2;
 };
 
 // r[i], by halving: registers have no index.
@@ -281,11 +320,10 @@ __device__ __forceinline__ void stage16(char* buf, int lane, int chunk, uint32_t
 
 template <int Op, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    ssd_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_out, const GemmArgs a) {
+    ssd_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
   using S = GemmShape<Op, CG>;
   constexpr int kStages = S::kStages, kTileN = S::kTileN;
-  constexpr bool kAMn = Op == kOpDw, kBMn = Op == kOpDh || Op == kOpDw;
+  constexpr bool kBMn = is_back(Op);
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   char* out_buf = smem + kStages * S::kStage;
@@ -319,15 +357,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   stream_wait();
   const int n_active = a.hdr->n_active;
   const float scale_max = a.hdr->scale_max;
-  const GemmWork<Op, CG> work(a, n_active);
-  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  const GemmWork<Op, CG> work(a, n_active, static_cast<int>(blockIdx.x) / CG, static_cast<int>(gridDim.x) / CG);
 
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < work.count; t += step) {
+      for (int t = 0; ok && t < work.count; ++t) {
         const GemmTile tile = work.at(a, t);
         const int m0 = tile.m * S::kTileM + rank * 128, n0 = tile.n * kTileN + rank * S::kBRows;
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
@@ -340,18 +377,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const int k0 = kb * kBlockK;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], S::kStage * CG);
           const uint32_t bar = CG == 1 ? smem_addr(&full[s]) : cluster_addr(&full[s], 0);
-          if (kAMn) {
-            tma_load<CG>(pa, &map_a, m0, k0, bar);
-            tma_load<CG>(pa + 8192, &map_a, m0 + 64, k0, bar);
+          if (is_back(Op) && tile.dw) {
+            tma_load<CG>(pa, &maps.a2, m0, k0, bar);
+            tma_load<CG>(pa + 8192, &maps.a2, m0 + 64, k0, bar);
           } else {
-            tma_load<CG>(pa, &map_a, k0, m0, bar);
+            tma_load<CG>(pa, &maps.a, k0, m0, bar);
           }
           if (kBMn) {
-            const int y = k0 + (Op == kOpDh ? a.v0 : 0);
+            const CUtensorMap* map = tile.dw ? &maps.b2 : &maps.b;
+            const int y = k0 + (tile.dw ? 0 : a.v0);
 #pragma unroll
-            for (int j = 0; j < S::kBRows / 64; ++j) tma_load<CG>(pb + j * 8192, &map_b, n0 + j * 64, y, bar);
+            for (int j = 0; j < S::kBRows / 64; ++j) tma_load<CG>(pb + j * 8192, map, n0 + j * 64, y, bar);
           } else {
-            tma_load<CG>(pb, &map_b, k0, a.v0 + n0, bar);
+            tma_load<CG>(pb, &maps.b, k0, a.v0 + n0, bar);
           }
           if (++s == kStages) {
             s = 0;
@@ -363,18 +401,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // D fp32, A and B bf16, majorness, N / 8, M / 16
-      constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u) |
+      constexpr uint32_t shape = (1u << 4) | (1u << 7) | (1u << 10) | (kBMn ? 1u << 16 : 0u) |
                                  (static_cast<uint32_t>(kTileN / 8) << 17) |
                                  (static_cast<uint32_t>(S::kTileM / 16) << 24);
       int s = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < work.count; t += step) {
+      for (int t = 0; ok && t < work.count; ++t) {
         const GemmTile tile = work.at(a, t);
         if (tile.kb0 == tile.kb1) continue;
         if (!wait(&tempty[acc], acc_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * kAccCols;
+        const bool a_mn = is_back(Op) && tile.dw;
+        const uint32_t idesc = shape | (a_mn ? 1u << 15 : 0u);
+        const uint64_t a_step = (a_mn ? 2048 : 32) >> 4;
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
           if (!wait(&full[s], phase)) {
             ok = false;
@@ -382,10 +423,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           tc_fence_after();
           const uint32_t pa = smem_addr(smem + s * S::kStage);
-          const uint64_t da = operand_desc(pa, kAMn), db = operand_desc(pa + kATile, kBMn);
+          const uint64_t da = operand_desc(pa, a_mn), db = operand_desc(pa + kATile, kBMn);
 #pragma unroll
           for (int k = 0; k < kBlockK / 16; ++k)
-            mma_bf16<CG>(d, da + static_cast<uint64_t>(k * ((kAMn ? 2048 : 32) >> 4)),
+            mma_bf16<CG>(d, da + k * a_step,
                          db + static_cast<uint64_t>(k * ((kBMn ? 2048 : 32) >> 4)), idesc,
                          (kb > tile.kb0 || k > 0) ? 1u : 0u);
           mma_commit<CG>(&empty[s]);
@@ -405,7 +446,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     char* buf = out_buf + (warp - 2) * 2 * kOutBuf;
     int acc = 0, b = 0;
     uint32_t acc_phase = 0;
-    for (int t = first; t < work.count; t += step) {
+    for (int t = 0; t < work.count; ++t) {
       const GemmTile tile = work.at(a, t);
       if (tile.kb0 == tile.kb1) continue;
       const int row = tile.m * S::kTileM + rank * 128 + quad * 32 + lane;  // of the product
@@ -426,6 +467,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t src = tmem + acc * kAccCols + (static_cast<uint32_t>(quad * 32) << 16);
       float mx = -INFINITY, sum = 0.f;
+      const auto walk = [&](auto of_dw) {
+        constexpr bool kDw = decltype(of_dw)::value;
 #pragma unroll 1
       for (int c = 0; c < kTileN / 32; ++c) {
         uint32_t r[32];
@@ -468,12 +511,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-              tma_store(&map_out, tile.n * kTileN + (c >> 1) * 64, row0, buf + b * kOutBuf);
+              tma_store(&maps.out, tile.n * kTileN + (c >> 1) * 64, row0, buf + b * kOutBuf);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             b ^= 1;
           }
-        } else if (Op == kOpDh) {
+        } else if (!kDw) {
           if (tile.n * kTileN + c * 32 < a.D) {  // uniform over the warp
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
             __syncwarp();
@@ -485,9 +528,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (lane == 0) {
               const int x = tile.n * kTileN + c * 32, y = tile.slot * a.rows + row0;
               if (a.first)
-                tma_store(&map_out, x, y, buf + b * kOutBuf);
+                tma_store(&maps.out, x, y, buf + b * kOutBuf);
               else
-                tma_add(&map_out, x, y, buf + b * kOutBuf);
+                tma_add(&maps.out, x, y, buf + b * kOutBuf);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             b ^= 1;
@@ -512,7 +555,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               fence_proxy_async_shared();
               __syncwarp();
               if (lane == 0) {
-                tma_store(&map_out, tile.n * kTileN + (c >> 1) * 64, a.v0 + row0, buf + b * kOutBuf);
+                tma_store(&maps.out2, tile.n * kTileN + (c >> 1) * 64, a.v0 + row0, buf + b * kOutBuf);
                 asm volatile("cp.async.bulk.commit_group;" ::: "memory");
               }
               b ^= 1;
@@ -520,6 +563,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
       }
+      };
+      if (Op == kOpDw || (Op == kOpBack && tile.dw))
+        walk(std::true_type());
+      else
+        walk(std::false_type());
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {

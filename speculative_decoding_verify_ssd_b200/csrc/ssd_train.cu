@@ -172,6 +172,7 @@ static bool tile_map(CUtensorMap* m, const void* base, bool fp32, long long cols
 }
 
 constexpr long long kPieceBytes = 256ll << 20;  // of the gradient's logits, kept at a time
+constexpr long long kBothBytes = 128ll << 20;  // a piece of G that L2 holds
 constexpr int kMaxSlots = 32;
 
 // Sizes of one call, and where its workspace holds what.
@@ -181,6 +182,7 @@ struct LinearPlan {
   int tiles;         // vocabulary tiles of the forward call
   int piece;         // vocabulary of one piece of the gradient
   int slots;         // splits of a piece's k axis in dh
+  bool both;         // dh and dw in one launch
   size_t hdr, index, target, scale, lse, zt, h, part, g, dh, total;
 };
 
@@ -193,17 +195,32 @@ static LinearPlan linear_plan(int N, int D, int V, bool grad) {
   const long long v_up = (V + 255ll) / 256 * 256;  // dw's tiles are 256 high
   const long long fit = kPieceBytes / (2ll * p.rows) / 256 * 256;
   p.piece = static_cast<int>(fit < 256 ? 256 : (fit > v_up ? v_up : fit));
-  // Splits of k in dh: the fewest whole waves of tiles per split, each split of
-  // at least 8 blocks of k, few splits where they make no difference.
-  const int m_tiles = p.rows / tm, d_tiles = (D + tn - 1) / tn, groups = kSmCount / p.cg;
-  const int blocks = ((V < p.piece ? V : p.piece) + kBlockK - 1) / kBlockK;
-  const long long tiles = static_cast<long long>(m_tiles) * d_tiles;
-  double best = 1e30;
-  for (int k = 1; k <= kMaxSlots && (k == 1 || blocks / k >= 8); ++k) {
-    const double waves = static_cast<double>((tiles * k + groups - 1) / groups) / k * (1.0 + 0.01 * k);
-    if (waves < best) {
-      best = waves;
-      p.slots = k;
+  // One launch for dH and dW where L2 holds the piece of G that both read: 1024
+  // rows of 1024 over 32000 172 us against 178, 4096 of 512 over 16000 213
+  // against 237; but 4096 of 2048 over 32000 (250 MB) 1254 against 1234.  For
+  // single CTAs also where L2 holds the weight (64 rows of 2048 over 128256: 441
+  // us with the loss, against 415).
+  p.both = 2ll * p.rows * p.piece <= kBothBytes && (p.cg == 2 || 2ll * V * D <= kBothBytes);
+  const long long dh_cols = p.both ? 256 : 128 * p.cg;
+  const long long v_piece = V < p.piece ? V : p.piece, d_tiles = (D + dh_cols - 1) / dh_cols, groups = kSmCount / p.cg;
+  const long long dh_tiles = p.rows / tm * d_tiles, dw_tiles = (v_piece + tm - 1) / tm * d_tiles;
+  const long long blocks = (v_piece + kBlockK - 1) / kBlockK, dw_blocks = (N + kBlockK - 1) / kBlockK;
+  p.slots = 1;
+  if (p.both) {
+    // splits of k in dH: the fewest that leave no dH tile with more than half of a group's work
+    const long long least = p.cg == 1 ? GemmWork<kOpBack, 1>::dw_cost(static_cast<int>(dw_blocks))
+                                      : GemmWork<kOpBack, 2>::dw_cost(static_cast<int>(dw_blocks));
+    const long long half = (dh_tiles * blocks + dw_tiles * least) / (2 * groups);
+    while (p.slots < kMaxSlots && blocks / (p.slots + 1) >= 8 && blocks > half * p.slots) ++p.slots;
+  } else {
+    // the fewest whole waves of tiles per split, few splits where they make no difference
+    double best = 1e30;
+    for (int k = 1; k <= kMaxSlots && (k == 1 || blocks / k >= 8); ++k) {
+      const double waves = static_cast<double>((dh_tiles * k + groups - 1) / groups) / k * (1.0 + 0.01 * k);
+      if (waves < best) {
+        best = waves;
+        p.slots = k;
+      }
     }
   }
   size_t off = 0;
@@ -231,12 +248,11 @@ static LinearPlan linear_plan(int N, int D, int V, bool grad) {
 }
 
 template <int Op, int CG>
-static ssd_status launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a,
-                              long long most_tiles, cudaStream_t stream) {
+static ssd_status launch_gemm(const GemmMaps& maps, const GemmArgs& a, long long most_tiles, cudaStream_t stream) {
   const long long fit = kSmCount / CG;
   const long long groups = most_tiles < fit ? most_tiles : fit;
   return launch_dependent(&ssd_gemm_kernel<Op, CG>, dim3(static_cast<unsigned>(groups * CG)), kGemmThreads,
-                          GemmShape<Op, CG>::kSmem, CG, stream, ma, mb, mo, a);
+                          GemmShape<Op, CG>::kSmem, CG, stream, maps, a);
 }
 
 static ssd_status check_linear(int dtype, int n_batch, int rows_per_batch, int D, int V, int64_t batch_stride,
@@ -291,16 +307,16 @@ static GemmArgs gemm_args(const LinearPlan& p, char* ws, int V, int D) {
 template <int CG>
 static ssd_status linear_forward(const LinearPlan& p, char* ws, const void* weight, long long ws_bytes_row, int N, int D,
                                  int V, float* loss, float* lse, int32_t* status, cudaStream_t stream) {
-  CUtensorMap mh, mw;
-  if (!tile_map(&mh, ws + p.h, false, D, N, 2ll * D, 128) ||
-      !tile_map(&mw, weight, false, D, V, ws_bytes_row, GemmShape<kOpLse, CG>::kBRows))
+  GemmMaps maps = {};
+  if (!tile_map(&maps.a, ws + p.h, false, D, N, 2ll * D, 128) ||
+      !tile_map(&maps.b, weight, false, D, V, ws_bytes_row, GemmShape<kOpLse, CG>::kBRows))
     return SSD_ERR_CUDA;
   GemmArgs g = gemm_args(p, ws, V, D);
   g.v_count = V;
   g.zt = reinterpret_cast<float*>(ws + p.zt);
   g.part = reinterpret_cast<float2*>(ws + p.part);
   const long long most = static_cast<long long>(p.rows / GemmShape<kOpLse, CG>::kTileM) * p.tiles;
-  const ssd_status st = launch_gemm<kOpLse, CG>(mh, mw, mw, g, most, stream);
+  const ssd_status st = launch_gemm<kOpLse, CG>(maps, g, most, stream);
   if (st != SSD_OK) return st;
   return launch_dependent(&ssd_linear_join_kernel, dim3(static_cast<unsigned>((N + kJoinRows - 1) / kJoinRows)),
                           kJoinThreads, 0, 0, stream, g.hdr, static_cast<const float2*>(g.part), p.rows, p.tiles,
@@ -313,34 +329,37 @@ static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* wei
                                   int D, int V, void* grad_hidden, void* grad_weight, int32_t* status,
                                   cudaStream_t stream) {
   using S = GemmShape<kOpGrad, CG>;
-  using W = GemmShape<kOpDw, CG>;
-  CUtensorMap h_k, h_mn, w_k, w_mn, g_out, g_k, g_mn, dh_out, dw_out;
+  using W = GemmShape<kOpBack, CG>;
   // The maps end at row N: what a tile reads behind it is zero and costs no traffic.
-  if (!tile_map(&h_k, ws + p.h, false, D, N, 2ll * D, 128) ||
-      !tile_map(&h_mn, ws + p.h, false, D, N, 2ll * D, 64) ||
-      !tile_map(&w_k, weight, false, D, V, ws_bytes_row, S::kBRows) ||
-      !tile_map(&w_mn, weight, false, D, V, ws_bytes_row, 64) ||
-      !tile_map(&g_out, ws + p.g, false, p.piece, N, 2ll * p.piece, 32) ||
-      !tile_map(&g_k, ws + p.g, false, p.piece, N, 2ll * p.piece, 128) ||
-      !tile_map(&g_mn, ws + p.g, false, p.piece, N, 2ll * p.piece, 64) ||
-      !tile_map(&dh_out, ws + p.dh, true, D, static_cast<long long>(p.rows) * p.slots, 4ll * D, 32) ||
-      !tile_map(&dw_out, grad_weight, false, D, V, 2ll * D, 32))
+  GemmMaps grad = {}, back = {};
+  if (!tile_map(&grad.a, ws + p.h, false, D, N, 2ll * D, 128) ||
+      !tile_map(&grad.b, weight, false, D, V, ws_bytes_row, S::kBRows) ||
+      !tile_map(&grad.out, ws + p.g, false, p.piece, N, 2ll * p.piece, 32) ||
+      !tile_map(&back.a, ws + p.g, false, p.piece, N, 2ll * p.piece, 128) ||
+      !tile_map(&back.b, weight, false, D, V, ws_bytes_row, 64) ||
+      !tile_map(&back.out, ws + p.dh, true, D, static_cast<long long>(p.rows) * p.slots, 4ll * D, 32) ||
+      !tile_map(&back.a2, ws + p.g, false, p.piece, N, 2ll * p.piece, 64) ||
+      !tile_map(&back.b2, ws + p.h, false, D, N, 2ll * D, 64) ||
+      !tile_map(&back.out2, grad_weight, false, D, V, 2ll * D, 32))
     return SSD_ERR_CUDA;
   GemmArgs g = gemm_args(p, ws, V, D);
   g.scale = reinterpret_cast<const float*>(ws + p.scale);
   g.lse = reinterpret_cast<const float*>(ws + p.lse);
   g.slots = p.slots;
-  const long long m_tiles = p.rows / S::kTileM, d_tiles = (D + S::kTileN - 1) / S::kTileN;
+  const long long m_tiles = p.rows / S::kTileM, d_tiles = (D + W::kTileN - 1) / W::kTileN;
+  const long long dh_cols = p.both ? W::kTileN : GemmShape<kOpDh, CG>::kTileN;
   for (long long v0 = 0; v0 < V; v0 += p.piece) {
     g.v0 = static_cast<int>(v0);
     g.v_count = static_cast<int>(V - v0 < p.piece ? V - v0 : p.piece);
     g.first = v0 == 0;
     const long long v_tiles = (g.v_count + S::kTileN - 1) / S::kTileN;
-    ssd_status st = launch_gemm<kOpGrad, CG>(h_k, w_k, g_out, g, m_tiles * v_tiles, stream);
-    if (st == SSD_OK) st = launch_gemm<kOpDh, CG>(g_k, w_mn, dh_out, g, m_tiles * d_tiles * p.slots, stream);
+    ssd_status st = launch_gemm<kOpGrad, CG>(grad, g, m_tiles * v_tiles, stream);
+    const long long dh_most = m_tiles * p.slots * ((D + dh_cols - 1) / dh_cols);
+    const long long dw_most = (g.v_count + W::kTileM - 1ll) / W::kTileM * d_tiles;
     if (st == SSD_OK)
-      st = launch_gemm<kOpDw, CG>(g_mn, h_mn, dw_out, g,
-                                   (g.v_count + W::kTileM - 1ll) / W::kTileM * ((D + W::kTileN - 1) / W::kTileN), stream);
+      st = p.both ? launch_gemm<kOpBack, CG>(back, g, dh_most + dw_most, stream)
+                  : launch_gemm<kOpDh, CG>(back, g, dh_most, stream);
+    if (st == SSD_OK && !p.both) st = launch_gemm<kOpDw, CG>(back, g, dw_most, stream);
     if (st != SSD_OK) return st;
   }
   const dim3 grid(static_cast<unsigned>(N), static_cast<unsigned>((D / 4 + kDhThreads - 1) / kDhThreads));
