@@ -169,7 +169,7 @@ __device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, co
                : "memory");
 }
 
-// 32 consecutive accumulator columns of the warp's 32 lanes.
+// Starts the load of 32 consecutive accumulator columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -179,7 +179,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// The loads above have arrived: r has its values behind this.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // mbar_try_wait whose acquire reaches the other CTA of the pair.
@@ -467,12 +476,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       tc_fence_after();
       const uint32_t src = tmem + acc * kAccCols + (static_cast<uint32_t>(quad * 32) << 16);
       float mx = -INFINITY, sum = 0.f;
-      const auto walk = [&](auto of_dw) {
+      const auto chunk = [&](auto of_dw, int c, uint32_t (&r)[32]) {
         constexpr bool kDw = decltype(of_dw)::value;
-#pragma unroll 1
-      for (int c = 0; c < kTileN / 32; ++c) {
-        uint32_t r[32];
-        tmem_load32(src + c * 32, r);
         if (Op == kOpLse) {
           if (c * 32 + 32 > n_valid) {
 #pragma unroll
@@ -562,7 +567,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
           }
         }
-      }
+      };
+      // 32 columns at a time, the next ones on their way
+      const auto walk = [&](auto of_dw) {
+        uint32_t r0[32], r1[32];
+        tmem_load32(src, r0);
+#pragma unroll 1
+        for (int c = 0; c < kTileN / 32; c += 2) {
+          tmem_wait(r0);
+          tmem_load32(src + (c + 1) * 32, r1);
+          chunk(of_dw, c, r0);
+          tmem_wait(r1);
+          if (c + 2 < kTileN / 32) tmem_load32(src + (c + 2) * 32, r0);
+          chunk(of_dw, c + 1, r1);
+        }
       };
       if (Op == kOpDw || (Op == kOpBack && tile.dw))
         walk(std::true_type());
