@@ -7,6 +7,10 @@
 //   grad  G = s (softmax(z) - onehot)  in bf16, one piece of the vocabulary at a time
 //   back  dH += G W            -> fp32, one slot per split of the piece
 //         dW = G^T H           -> bf16; the tiles of both in one launch, or of one of them
+// Measured at 4096 rows of 2048 over 128256 under the power cap: lse 1366
+// TFLOP/s, grad 1202 (it writes 1 GB of G and forms the exponentials), dh and dw
+// 1230-1330; cuBLAS sustains 1399.  At 64 rows the weight's bytes bound lse, grad
+// and dh (5.3-6.4 TB/s) and the written gradient dw (5.3 TB/s).
 #pragma once
 
 #include <cuda.h>

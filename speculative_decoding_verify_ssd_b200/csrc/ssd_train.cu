@@ -195,11 +195,11 @@ static LinearPlan linear_plan(int N, int D, int V, bool grad) {
   const long long v_up = (V + 255ll) / 256 * 256;  // dw's tiles are 256 high
   const long long fit = kPieceBytes / (2ll * p.rows) / 256 * 256;
   p.piece = static_cast<int>(fit < 256 ? 256 : (fit > v_up ? v_up : fit));
-  // One launch for dH and dW where L2 holds the piece of G that both read: 1024
-  // rows of 1024 over 32000 172 us against 178, 4096 of 512 over 16000 213
-  // against 237; but 4096 of 2048 over 32000 (250 MB) 1254 against 1234.  For
-  // single CTAs also where L2 holds the weight (64 rows of 2048 over 128256: 441
-  // us with the loss, against 415).
+  // One launch for dH and dW where L2 holds the piece of G that both read: both
+  // gradients of 5 rows of 512 over 5003 22.6 us against 24.6, of 384 of 2048 over
+  // 32000 171 against 176, most sizes within 1%; but 2048 of 2048 over 128256 (two
+  // pieces of 256 MB) 2503 against 2328.  For single CTAs also where L2 holds the
+  // weight (64 rows of 2048 over 128256 294 against 289).
   p.both = 2ll * p.rows * p.piece <= kBothBytes && (p.cg == 2 || 2ll * V * D <= kBothBytes);
   const long long dh_cols = p.both ? 256 : 128 * p.cg;
   const long long v_piece = V < p.piece ? V : p.piece, d_tiles = (D + dh_cols - 1) / dh_cols, groups = kSmCount / p.cg;

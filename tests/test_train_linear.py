@@ -104,7 +104,8 @@ def test_sizes(N, D, V):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("N,D,V", [(5, 2048, 32003), (64, 1024, 128256), (1000, 256, 20011), (640, 2048, 4096)])
+@pytest.mark.parametrize("N,D,V", [(5, 2048, 32003), (64, 1024, 128256), (1000, 256, 20011), (640, 2048, 4096),
+                                    (3, 8192, 1025)])
 def test_larger(N, D, V):
     hidden, weight, targets = linear_case((N,), D, V, N, keep=0.7)
     check(hidden, weight, targets, torch.rand(N, device="cuda") + 0.5)
