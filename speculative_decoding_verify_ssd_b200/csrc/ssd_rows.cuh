@@ -53,7 +53,7 @@ struct Elem<uint16_t> {
   static constexpr int kVec = 8;
   static __device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static __device__ __forceinline__ uint16_t neg_inf() { return 0xFF80u; }
-  // round to nearest even; the callers' values are finite
+  // round to nearest even
   static __device__ __forceinline__ uint16_t from_float(float f) {
     uint16_t h;
     asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(f));
@@ -67,9 +67,6 @@ struct Elem<uint16_t> {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
   }
   static __device__ __forceinline__ void unpack2(const uint4& v, f32x2 (&f)[4]) {
     f[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x)), f[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
@@ -194,16 +191,6 @@ struct OpMax {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
   __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
 };
-struct OpMaxNan {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmax_nan(a, b); }
-};
-struct OpOr {
-  __device__ __forceinline__ int operator()(int a, int b) const { return a | b; }
-};
-
-// (reference, sum) stands for sum * exp(reference), natural units; its
-// logarithm.  A sum of 0 stands for nothing.
-__device__ __forceinline__ double lse_of(double ref, double sum) { return sum > 0.0 ? ref + log(sum) : -INFINITY; }
 
 // The largest of a warp's values, NaN when any is (made the canonical one,
 // whose key is the largest).
