@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -600,6 +601,7 @@ def _scratch(workspace, nbytes: int, dev):
     return workspace
 
 
+@functools.lru_cache(maxsize=1024)
 def teacher_top_workspace_bytes(rows: int, V: int, dtype: int, M: int) -> int:
     return int(load().ssd_teacher_top_workspace_bytes(rows, V, dtype, M))
 
@@ -615,7 +617,7 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, workspace: Opt
     wide = lead + (max(M, 0),)
 
     def call(st):
-        ws = _scratch(workspace, load().ssd_teacher_top_workspace_bytes(nb * rpb, V, dt, M), dev)
+        ws = _scratch(workspace, teacher_top_workspace_bytes(nb * rpb, V, dt, M), dev)
         values = torch.empty(wide, dtype=torch.float32, device=dev)
         lse = torch.empty(lead, dtype=torch.float32, device=dev)
         r = TeacherTop(tokens=torch.empty_like(values, dtype=torch.int32), values=values, lse=lse,
@@ -678,6 +680,7 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
     return _launch(index, stream, call)
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_ce_workspace_bytes(N: int, D: int, V: int, grad: bool) -> int:
     return int(load().ssd_linear_ce_workspace_bytes(N, D, V, int(grad)))
 
