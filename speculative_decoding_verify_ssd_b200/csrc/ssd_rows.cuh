@@ -257,59 +257,37 @@ __device__ __forceinline__ float slice_max(const uint4* data, int count) {
 }
 
 // The gradient outside the atoms, k 2^((f - ref) c), of a staged vector.
-template <typename TIn>
-struct GradOf;
-// Rounded to bf16: |k| goes into the exponent, and where |ref c| is moderate the
-// product f c may carry c's rounding (2^-24 |f c|, below 2^-13).
-template <>
-struct GradOf<uint16_t> {
-  f32x2 c2, d2, r2;
-  uint32_t sign;
-  bool far;
-  __device__ __forceinline__ GradOf(float k, float ref, float c) {
-    far = !(fabsf(ref * c) <= 1024.f);
-    const float d = log2f(fabsf(k)) - (far ? 0.f : ref * c);
-    c2 = f2_pack(c, c);
-    d2 = f2_pack(d, d);
-    r2 = f2_pack(-ref, -ref);
-    sign = k < 0.f ? 0x80008000u : 0u;
-  }
-  __device__ __forceinline__ uint32_t pair(f32x2 f) const {
+//
+// Rounded to bf16, |k| goes into the exponent (d = log2 |k|) and its sign into
+// the conversion; where |ref c| is moderate (kFar false) so does -ref c: the
+// product f c then carries c's rounding (2^-24 |f c|, below 2^-13).
+struct GradScale {
+  float k, d, ref, c;
+};
+template <typename TIn, bool kNegative, bool kFar>
+__device__ __forceinline__ uint4 gradient_of(const uint4& v, const GradScale& g) {
+  constexpr int kPairs = Elem<TIn>::kVec / 2;
+  const f32x2 c2 = f2_pack(g.c, g.c), r2 = f2_pack(-g.ref, -g.ref);
+  f32x2 f[kPairs];
+  uint32_t out[4];
+  Elem<TIn>::unpack2(v, f);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
     float x, y;
-    f2_unpack(f2_fma(f, c2, d2), x, y);
-    return Elem<uint16_t>::pack2(ex2(x), ex2(y)) ^ sign;
-  }
-  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
-    f32x2 f[4];
-    Elem<uint16_t>::unpack2(v, f);
-    if (far) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = f2_add(f[i], r2);
+    if (sizeof(TIn) == 2) {
+      const f32x2 d2 = f2_pack(g.d, g.d);
+      f2_unpack(f2_fma(kFar ? f2_add(f[i], r2) : f[i], c2, d2), x, y);
+      out[i] = kNegative ? Elem<uint16_t>::pack2(-ex2(x), -ex2(y)) : Elem<uint16_t>::pack2(ex2(x), ex2(y));
+    } else {
+      const f32x2 k2 = f2_pack(g.k, g.k);
+      f2_unpack(f2_mul(f2_add(f[i], r2), c2), x, y);
+      f2_unpack(f2_mul(f2_pack(ex2(x), ex2(y)), k2), x, y);
+      out[2 * i] = __float_as_uint(x);
+      out[2 * i + 1] = __float_as_uint(y);
     }
-    return make_uint4(pair(f[0]), pair(f[1]), pair(f[2]), pair(f[3]));
   }
-};
-template <>
-struct GradOf<float> {
-  f32x2 k2, r2, c2;
-  __device__ __forceinline__ GradOf(float k, float ref, float c) {
-    k2 = f2_pack(k, k);
-    r2 = f2_pack(-ref, -ref);
-    c2 = f2_pack(c, c);
-  }
-  __device__ __forceinline__ uint4 operator()(const uint4& v) const {
-    f32x2 f[2];
-    float g[4];
-    Elem<float>::unpack2(v, f);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x, y;
-      f2_unpack(f2_mul(f2_add(f[e], r2), c2), x, y);
-      f2_unpack(f2_mul(f2_pack(ex2(x), ex2(y)), k2), g[2 * e], g[2 * e + 1]);
-    }
-    return Elem<float>::pack(g);
-  }
-};
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
 
 // What one warp, and then one CTA, of a distillation row found: sums of
 // exponentials of its tail logits and atoms around their maxima (tail_sum NaN:
@@ -327,6 +305,14 @@ struct DistillTeacher {
   double top, total;  // top in units of logits / T
   float inv_total, p_tail;
   int flags;
+};
+
+// The joined row, as the gradient needs it.
+struct DistillJoin {
+  GradScale scale;       // outside the atoms; k 0: none, or a void row
+  float at_top, weight;  // on an atom: weight * (2^((z - at_top) c) / total - p)
+  float total;
+  int bad, far;
 };
 
 struct DistillArgs {
@@ -358,9 +344,9 @@ struct DistillArgs {
 // Each of a slice's phases (load, maximum, exponentials, exchange, exponentials
 // again, store) is bound by something else, and they follow one another in a
 // CTA: four CTAs of 52 KB slices per SM overlap part of them.  384 rows of
-// 128256 bf16 with gradient take 53.4 us (3.7 TB/s of logits and gradient, 56%
-// of the copy rate; issue 44%, exp2 pipe 45%), 2048 rows of 151936 296 us
-// (4.2 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
+// 128256 bf16 with gradient take 52.4 us (3.8 TB/s of logits and gradient, 58%
+// of the copy rate; issue 44%, exp2 pipe 45%), 2048 rows of 151936 289 us
+// (4.3 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
 // the next row, and a gradient stored in bulk all measured slower.
 // ---------------------------------------------------------------------------
 template <typename TIn>
@@ -373,6 +359,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
   __shared__ DistillPart warps[kRowWarps];
   __shared__ DistillPart parts[kMaxRowCluster];  // the cluster's, written by their CTAs
   __shared__ DistillTeacher teacher;
+  __shared__ DistillJoin join;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), C = static_cast<int>(cluster.num_blocks());
@@ -511,54 +498,67 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
   }
   cluster.sync();
 
-  // Every warp joins the cluster's parts for itself, in the same order, in 32
+  // One warp joins the cluster's parts, in the same order in every CTA, in 32
   // bits: all the gradient needs.
   float4 q = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-  if (lane < C) q = *reinterpret_cast<const float4*>(&parts[lane]);
-  const float tail_max = warp_max_nan(q.x), atom_max = warp_max_nan(q.z);
-  const float tail = warp_sum8(q.y == 0.f ? 0.f : q.y * ex2((q.x - tail_max) * c));  // NaN stays
-  const float atom = warp_sum8(q.w == 0.f ? 0.f : q.w * ex2((q.z - atom_max) * c));
-  const float at_top = fmaxf(tail_max, atom_max);
-  const float tail_share = tail_max > -INFINITY ? tail * ex2((tail_max - at_top) * c) : 0.f;
-  const float total = tail_share + (atom_max > -INFINITY ? atom * ex2((atom_max - at_top) * c) : 0.f);
-  const bool bad = !(tail >= 0.f) || !(total > 0.f);  // a void row; every logit -inf
-
-  const float w = scale * static_cast<float>(invT);
+  float tail_max = -INFINITY, atom_max = -INFINITY, at_top = -INFINITY;
+  bool bad = false;
+  if (warp == 0) {
+    if (lane < C) q = *reinterpret_cast<const float4*>(&parts[lane]);
+    tail_max = warp_max_nan(q.x);
+    atom_max = warp_max_nan(q.z);
+    const float tail = warp_sum8(q.y == 0.f ? 0.f : q.y * ex2((q.x - tail_max) * c));  // NaN stays
+    const float atom = warp_sum8(q.w == 0.f ? 0.f : q.w * ex2((q.z - atom_max) * c));
+    at_top = fmaxf(tail_max, atom_max);
+    const float tail_share = tail_max > -INFINITY ? tail * ex2((tail_max - at_top) * c) : 0.f;
+    const float total = tail_share + (atom_max > -INFINITY ? atom * ex2((atom_max - at_top) * c) : 0.f);
+    bad = !(tail >= 0.f) || !(total > 0.f);  // a void row; every logit -inf
+    if (lane == 0) {
+      const float w = scale * static_cast<float>(invT);
+      const float k = bad || !(tail > 0.f) ? 0.f : w * (tail_share / total - teacher.p_tail) / tail;
+      const float ref = tail > 0.f ? tail_max : 0.f;
+      const bool far = !(fabsf(ref * c) <= 1024.f);
+      join = DistillJoin{{k, log2f(fabsf(k)) - (far ? 0.f : ref * c), ref, c}, at_top, w, total, bad, far};
+    }
+  }
   if (dst) {
-    const float k = bad || !(tail > 0.f) ? 0.f : w * (tail_share / total - teacher.p_tail) / tail;
-    const float r0 = tail > 0.f ? tail_max : 0.f;
+    __syncthreads();
+    const DistillJoin j = join;
     // whole vectors only where the row's places in both tensors agree modulo 16 bytes
     const bool same = ((reinterpret_cast<uintptr_t>(dst) ^ reinterpret_cast<uintptr_t>(src)) & 15u) == 0;
     const int shift = s.first * VE - s.head;  // the token of the slice's first place
     const int whole0 = same ? (shift < 0 ? 1 : 0) : s.count, whole1 = same ? min(s.count, (a.V - shift) / VE) : s.count;
-    const GradOf<TIn> gradient(k, r0, c);
-    if (k == 0.f) {  // also a void row, whose logits may be NaN
-#pragma unroll 2
-      for (int i = whole0 + tid; i < whole1; i += kRowThreads)
-        *reinterpret_cast<uint4*>(dst + shift + i * VE) = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-#pragma unroll 2
-      for (int i = whole0 + tid; i < whole1; i += kRowThreads)
-        *reinterpret_cast<uint4*>(dst + shift + i * VE) = gradient(data[i]);
-    }
     // the vectors at the row's edges, or all of them
-    const auto by_element = [&](int i) {
-      const uint4 g = k == 0.f ? make_uint4(0u, 0u, 0u, 0u) : gradient(data[i]);
+    const auto by_element = [&](int i, const uint4& g) {
       const TIn* e = reinterpret_cast<const TIn*>(&g);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const int v = shift + i * VE + j;
-        if (v >= 0 && v < a.V) dst[v] = e[j];
+      for (int n = 0; n < VE; ++n) {
+        const int v = shift + i * VE + n;
+        if (v >= 0 && v < a.V) dst[v] = e[n];
       }
     };
-    if (same) {
-      if (tid == 0 && whole0 == 1 && s.count > 0) by_element(0);
-      if (tid == 32 && whole1 < s.count && whole1 >= whole0) by_element(whole1);
-    } else {
-      for (int i = tid; i < s.count; i += kRowThreads) by_element(i);
-    }
+    const auto write = [&](auto value) {
+#pragma unroll 2
+      for (int i = whole0 + tid; i < whole1; i += kRowThreads) *reinterpret_cast<uint4*>(dst + shift + i * VE) = value(i);
+      if (same) {
+        if (tid == 0 && whole0 == 1 && s.count > 0) by_element(0, value(0));
+        if (tid == 32 && whole1 < s.count && whole1 >= whole0) by_element(whole1, value(whole1));
+      } else {
+        for (int i = tid; i < s.count; i += kRowThreads) by_element(i, value(i));
+      }
+    };
+    if (j.scale.k == 0.f)  // also a void row, whose logits may be NaN
+      write([](int) { return make_uint4(0u, 0u, 0u, 0u); });
+    else if (sizeof(TIn) == 2 && j.far)
+      j.scale.k < 0.f ? write([&](int i) { return gradient_of<TIn, true, true>(data[i], j.scale); })
+                      : write([&](int i) { return gradient_of<TIn, false, true>(data[i], j.scale); });
+    else if (sizeof(TIn) == 2 && j.scale.k < 0.f)
+      write([&](int i) { return gradient_of<TIn, true, false>(data[i], j.scale); });
+    else
+      write([&](int i) { return gradient_of<TIn, false, false>(data[i], j.scale); });
     __syncthreads();  // the atoms' places are written after the vectors that hold them
-    if (mine && !bad) dst[id] = Elem<TIn>::from_float(w * (ex2((z_atom - at_top) * c) / total - p));
+    if (mine && !j.bad)
+      dst[id] = Elem<TIn>::from_float(j.weight * (ex2((z_atom - j.at_top) * c) / j.total - p));
   }
   if (rank == 0 && warp == 0) {
     // The loss is made of differences of logarithms: 64 bits.
