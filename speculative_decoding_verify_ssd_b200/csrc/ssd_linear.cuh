@@ -138,13 +138,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         : "memory");
 }
 
-// The address of a shared-memory place in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
-}
-
 // Tile load into this CTA's shared memory; the bytes are counted on the
 // barrier at cluster address `bar` (the pair's first CTA when CG = 2).
 template <int CG>
@@ -195,19 +188,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// mbar_try_wait whose acquire reaches the other CTA of the pair.
-__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
-      : "memory");
-  return done != 0;
-}
-
 // A wait of one of the kernel's roles.  Once one has given up, the kernel's
 // other waits in this CTA give up too, and the call is flagged.
 template <int CG>
@@ -215,7 +195,7 @@ struct GemmWait {
   volatile int* abort;
   int32_t* error;
   static __device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
-    return CG == 1 ? mbar_try_wait(bar, parity, kSuspendHintNs) : mbar_try_wait_pair(bar, parity);
+    return CG == 1 ? mbar_try_wait(bar, parity, kSuspendHintNs) : mbar_try_wait_cluster(bar, parity);
   }
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     if (poll(bar, parity)) return true;

@@ -10,6 +10,7 @@
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/ssd.h"
@@ -153,6 +154,43 @@ __device__ __forceinline__ void slice_load(const TIn* row, int V, const Slice& s
   }
 }
 
+// The address of a shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+
+// mbar_try_wait whose acquire reaches the other CTAs of the cluster.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  return done != 0;
+}
+
+// Stores into another CTA's shared memory whose bytes are counted on that CTA's
+// barrier: the receiver waits for them alone, and the sender for nothing.
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float a, float b, float c, float d) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, double a, double b) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f64 [%0], {%1, %2}, [%3];" ::"r"(to), "d"(a),
+               "d"(b), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, int a) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(a), "r"(bar)
+               : "memory");
+}
+
 // Waits for the slice's bytes; a barrier of the CTA (one warp polls, the others
 // stand at the barrier).  A wait that gives up waits once more (the copies still
 // target this CTA's shared memory) before the row is flagged.
@@ -163,6 +201,19 @@ __device__ __forceinline__ int slice_wait(uint64_t* bar, uint32_t parity) {
     if (late) (void)mbar_wait_bounded(bar, parity, kRowWaitNs);
   }
   return __syncthreads_or(late) ? SSD_ROW_DEVICE_TIMEOUT : 0;
+}
+
+// Waits for the cluster's parts.  Its limit is twice slice_wait's, the longest
+// that another CTA of the cluster can be behind: a CTA that gives up here has
+// no store still coming.
+__device__ __forceinline__ int parts_wait(uint64_t* bar) {
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long t0 = global_ns();
+    do {
+      if (mbar_try_wait_cluster(bar, 0)) return i == 0 ? 0 : SSD_ROW_DEVICE_TIMEOUT;
+    } while (global_ns() - t0 < kRowWaitNs);
+  }
+  return SSD_ROW_DEVICE_TIMEOUT;
 }
 
 // ---------------------------------------------------------------------------
@@ -344,16 +395,16 @@ struct DistillArgs {
 // Each of a slice's phases (load, maximum, exponentials, exchange, exponentials
 // again, store) is bound by something else, and they follow one another in a
 // CTA: four CTAs of 52 KB slices per SM overlap part of them.  384 rows of
-// 128256 bf16 with gradient take 52.4 us (3.8 TB/s of logits and gradient, 58%
-// of the copy rate; issue 44%, exp2 pipe 45%), 2048 rows of 151936 289 us
-// (4.3 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
+// 128256 bf16 with gradient take 47.6 us (4.1 TB/s of logits and gradient, 63%
+// of the copy rate; issue 44%, exp2 pipe 47%), 2048 rows of 151936 257 us
+// (4.9 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
 // the next row, and a gradient stored in bulk all measured slower.
 // ---------------------------------------------------------------------------
 template <typename TIn>
 __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const DistillArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, parts_bar;
   __shared__ __align__(16) int32_t ids[SSD_MAX_TOP];
   __shared__ float atoms[SSD_MAX_TOP];
   __shared__ DistillPart warps[kRowWarps];
@@ -390,14 +441,22 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     return;
   }
 
-  cluster.barrier_arrive();  // this CTA runs: the others may write into it
+  // The parts that this CTA waits for: everyone's sums where it forms a
+  // gradient, the loss terms too in the first.
+  const uint32_t parts_bytes = (rank == 0 ? 36u : (dst ? 16u : 0u)) * static_cast<uint32_t>(C);
   if (warp == kRowWarps - 1) {
     if (lane == 0) {
       mbar_init(&bar, 1);
+      mbar_init(&parts_bar, 1);
       mbar_init_fence();
+      mbar_arrive_expect_tx(&parts_bar, parts_bytes);
     }
-    slice_load(src, a.V, s, data, &bar);
+    __syncwarp();
   }
+  // This CTA runs and has its barrier: the others may write into it.  (Relaxed:
+  // the barrier's own fence has published it.)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
   const double invT = a.inv_t;
   const float c = a.log2e_t;
   const float t = id >= 0 ? t_in : -INFINITY;
@@ -470,12 +529,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     if (lane == 0) warps[warp] = DistillPart{ref, sum, am, as, num, weight, flags};
   }
   __syncthreads();
-  cluster.barrier_wait();  // every CTA runs
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs
   if (warp == 0) {
-    // The CTA's part, written into every CTA of the cluster (its loss terms
-    // only into the first): a few remote stores, and after the barrier every
-    // read is local.  Reading the warps' parts remotely from every warp cost
-    // more than the sums themselves.
+    // The CTA's part, written into every CTA of the cluster (its loss terms only
+    // into the first).  Reading the warps' parts remotely from every warp cost
+    // more than the sums themselves; ordinary remote stores and a cluster barrier
+    // cost a fence: 289 us for 2048 rows of 151936 bf16 against 257.
     DistillPart q = {};
     if (lane < kRowWarps) q = warps[lane];
     float tm = q.tail_sum > 0.f ? q.tail_max : -INFINITY, am = q.atom_sum > 0.f ? q.atom_max : -INFINITY;
@@ -486,24 +545,25 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const float as = warp_sum8(q.atom_sum > 0.f ? q.atom_sum * ex2((q.atom_max - am) * c) : 0.f);
     const double num = warp_sum8(q.numer), weight = warp_sum8(q.weight);
     const DistillPart out = {tm, fl ? __int_as_float(0x7FC00000) : ts, am, as, num, weight, fl};
-    if (lane < C) {
-      DistillPart* to = cluster.map_shared_rank(&parts[0], lane) + rank;
-      *reinterpret_cast<float4*>(to) = make_float4(out.tail_max, out.tail_sum, out.atom_max, out.atom_sum);
+    if (lane < C && (lane == 0 || dst)) {
+      const uint32_t to = cluster_addr(&parts[rank], lane), on = cluster_addr(&parts_bar, lane);
+      st_async(to, on, out.tail_max, out.tail_sum, out.atom_max, out.atom_sum);
       if (lane == 0) {
-        to->numer = out.numer;
-        to->weight = out.weight;
-        to->flags = out.flags;
+        st_async(to + offsetof(DistillPart, numer), on, out.numer, out.weight);
+        st_async(to + offsetof(DistillPart, flags), on, out.flags);
       }
     }
   }
-  cluster.sync();
+  if (!dst && rank != 0) return;  // nobody writes into this CTA
 
   // One warp joins the cluster's parts, in the same order in every CTA, in 32
   // bits: all the gradient needs.
   float4 q = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
   float tail_max = -INFINITY, atom_max = -INFINITY, at_top = -INFINITY;
   bool bad = false;
+  int late = 0;
   if (warp == 0) {
+    late = parts_wait(&parts_bar);
     if (lane < C) q = *reinterpret_cast<const float4*>(&parts[lane]);
     tail_max = warp_max_nan(q.x);
     atom_max = warp_max_nan(q.z);
@@ -512,7 +572,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     at_top = fmaxf(tail_max, atom_max);
     const float tail_share = tail_max > -INFINITY ? tail * ex2((tail_max - at_top) * c) : 0.f;
     const float total = tail_share + (atom_max > -INFINITY ? atom * ex2((atom_max - at_top) * c) : 0.f);
-    bad = !(tail >= 0.f) || !(total > 0.f);  // a void row; every logit -inf
+    bad = !(tail >= 0.f) || !(total > 0.f) || late != 0;  // a void row; every logit -inf
     if (lane == 0) {
       const float w = scale * static_cast<float>(invT);
       const float k = bad || !(tail > 0.f) ? 0.f : w * (tail_share / total - teacher.p_tail) / tail;
@@ -569,7 +629,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const double atom_d =
         warp_sum8(on && q.w > 0.f ? static_cast<double>(q.w) * static_cast<double>(ex2((q.z - atom_max) * c)) : 0.0);
     const double num = warp_sum8(on ? own->numer : 0.0), weight = warp_sum8(on ? own->weight : 0.0);
-    int fl = __reduce_or_sync(0xFFFFFFFFu, on ? own->flags : 0);
+    int fl = __reduce_or_sync(0xFFFFFFFFu, on ? own->flags : 0) | late;
     // Both around the larger maximum; the tail's own logarithm is kept where its share underflows.
     const float other = tail_max > atom_max ? atom_max : tail_max;
     const double factor = other > -INFINITY ? exp((static_cast<double>(other) - static_cast<double>(at_top)) * invT) : 0.0;
