@@ -484,12 +484,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     sum = warp_sum(sum) + e_tail;
     if (lane == 0) teacher = DistillTeacher{at_top, static_cast<double>(sum), 1.f / sum, e_tail / sum, f};
   }
-  // Is a token there twice?  The other warps look, while the first is busy.
-  for (int m = tid - 32; m >= 0 && m < a.M; m += kRowThreads - 32) {
+  // Is a token there twice?  The cluster's CTAs share the tokens out, and in each
+  // the other warps look while the first is busy, every lane at four earlier ones.
+  for (int m = (warp - 1) * C + rank; warp > 0 && m < a.M; m += (kRowWarps - 1) * C) {
     const int want = ids[m];
     bool twice = false;
-#pragma unroll 4
-    for (int j = 0; j < m; j += 4) {
+    for (int j = 4 * lane; j < m; j += 128) {
       const int4 q = *reinterpret_cast<const int4*>(ids + j);
       twice |= q.x == want || (q.y == want && j + 1 < m) || (q.z == want && j + 2 < m) || (q.w == want && j + 3 < m);
     }

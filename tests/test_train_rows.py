@@ -297,6 +297,28 @@ def test_distill_masked_logits(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V, M", [(513, 256), (40001, 256), (140001, 256), (140001, 67), (401, 5)])
+def test_distill_token_twice_anywhere(V, M):
+    # one row for each pair of places that hold one token; every third row has none
+    pairs = [(i, j) for j in (1, 2, 3, 4, 31, 32, 63, 66, 127, 128, 131, 254, 255, M - 1) if j < M
+             for i in (0, 1, 3, j // 2, j - 1) if i < j]
+    rows = 3 * ((len(pairs) + 1) // 2)
+    g = torch.Generator().manual_seed(V + M)
+    tokens = torch.stack([torch.randperm(V, generator=g)[:M] for _ in range(rows)]).int()
+    want = torch.zeros(rows, dtype=torch.int32)
+    at = [r for r in range(rows) if r % 3 != 2][: len(pairs)]
+    for r, (i, j) in zip(at, pairs):
+        tokens[r, j] = tokens[r, i]
+        want[r] = ssd.ROW_BAD_TOKEN
+    z = torch.randn(rows, V, generator=g).bfloat16().cuda()
+    values = torch.randn(rows, M, generator=g).cuda()
+    r = ssd.ssd_distill(z, tokens.cuda(), values)
+    bad = want.cuda() != 0
+    assert torch.equal(r.status, want.cuda())
+    assert torch.equal(r.loss.isnan(), bad) and torch.equal((r.grad == 0).all(-1), bad)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("V", [513, 140001])
 def test_distill_void_rows(dtype, V):
