@@ -277,14 +277,13 @@ __device__ __forceinline__ void exp_sum(const uint4& v, f32x2 minus_ref, f32x2 c
   }
 }
 
-// The sum over a thread's vectors of the staged slice.
-template <typename TIn>
-__device__ __forceinline__ float slice_exp_sum(const uint4* data, int count, float ref, float c) {
+// The sum over a thread's vectors of the staged slice: i, i + kStride, ...
+template <typename TIn, int kStride = kRowThreads>
+__device__ __forceinline__ float slice_exp_sum(const uint4* data, int count, float ref, float c, int i = threadIdx.x) {
   const f32x2 r2 = f2_pack(-ref, -ref), c2 = f2_pack(c, c);
   f32x2 a0 = 0ull, a1 = 0ull;
-  int i = threadIdx.x;
-  for (; i + kRowThreads < count; i += 2 * kRowThreads) {
-    const uint4 u = data[i], w = data[i + kRowThreads];
+  for (; i + kStride < count; i += 2 * kStride) {
+    const uint4 u = data[i], w = data[i + kStride];
     exp_sum<TIn>(u, r2, c2, a0);
     exp_sum<TIn>(w, r2, c2, a1);
   }
@@ -294,12 +293,11 @@ __device__ __forceinline__ float slice_exp_sum(const uint4* data, int count, flo
   return x + y;
 }
 
-template <typename TIn>
-__device__ __forceinline__ float slice_max(const uint4* data, int count) {
+template <typename TIn, int kStride = kRowThreads>
+__device__ __forceinline__ float slice_max(const uint4* data, int count, int i = threadIdx.x) {
   float m = -INFINITY, m1 = -INFINITY;
-  int i = threadIdx.x;
-  for (; i + kRowThreads < count; i += 2 * kRowThreads) {
-    const uint4 u = data[i], w = data[i + kRowThreads];
+  for (; i + kStride < count; i += 2 * kStride) {
+    const uint4 u = data[i], w = data[i + kStride];
     m = fmax_nan(m, Elem<TIn>::vec_max(u));
     m1 = fmax_nan(m1, Elem<TIn>::vec_max(w));
   }
@@ -395,8 +393,8 @@ struct DistillArgs {
 // Each of a slice's phases (load, maximum, exponentials, exchange, exponentials
 // again, store) is bound by something else, and they follow one another in a
 // CTA: four CTAs of 52 KB slices per SM overlap part of them.  384 rows of
-// 128256 bf16 with gradient take 47.6 us (4.1 TB/s of logits and gradient, 63%
-// of the copy rate; issue 44%, exp2 pipe 47%), 2048 rows of 151936 257 us
+// 128256 bf16 with gradient take 45.3 us (4.4 TB/s of logits and gradient, 67%
+// of the copy rate; issue 50%, exp2 pipe 49%), 2048 rows of 151936 256 us
 // (4.9 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
 // the next row, and a gradient stored in bulk all measured slower.
 // ---------------------------------------------------------------------------
@@ -404,9 +402,9 @@ template <typename TIn>
 __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const DistillArgs a) {
   constexpr int VE = Elem<TIn>::kVec;
   extern __shared__ __align__(128) uint4 data[];
-  __shared__ uint64_t bar, parts_bar;
+  __shared__ uint64_t bars[kRowWarps], parts_bar;
   __shared__ __align__(16) int32_t ids[SSD_MAX_TOP];
-  __shared__ float atoms[SSD_MAX_TOP];
+  __shared__ float atoms[SSD_MAX_TOP], logits[SSD_MAX_TOP];  // the teacher's and, of this slice's, the student's
   __shared__ DistillPart warps[kRowWarps];
   __shared__ DistillPart parts[kMaxRowCluster];  // the cluster's, written by their CTAs
   __shared__ DistillTeacher teacher;
@@ -444,19 +442,23 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
   // The parts that this CTA waits for: everyone's sums where it forms a
   // gradient, the loss terms too in the first.
   const uint32_t parts_bytes = (rank == 0 ? 36u : (dst ? 16u : 0u)) * static_cast<uint32_t>(C);
-  if (warp == kRowWarps - 1) {
-    if (lane == 0) {
-      mbar_init(&bar, 1);
-      mbar_init(&parts_bar, 1);
-      mbar_init_fence();
-      mbar_arrive_expect_tx(&parts_bar, parts_bytes);
-    }
-    __syncwarp();
+  if (lane == 0) {
+    mbar_init(&bars[warp], 1);
+    if (warp == 0) mbar_init(&parts_bar, 1);
+    mbar_init_fence();
+    if (warp == 0) mbar_arrive_expect_tx(&parts_bar, parts_bytes);
   }
+  __syncwarp();
   // This CTA runs and has its barrier: the others may write into it.  (Relaxed:
   // the barrier's own fence has published it.)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  if (warp == kRowWarps - 1) slice_load(src, a.V, s, data, &bar);
+  // Each warp loads, patches and sums a piece of the slice of its own, and starts
+  // when that piece is there: 384 rows of 128256 bf16 45.3 us against 47.2 behind
+  // one barrier for the whole slice, 2048 of 151936 256 against 250.
+  const int each = (s.count + kRowWarps - 1) / kRowWarps, skip = min(warp * each, s.count);
+  const Slice piece = {s.head, s.first + skip, min(each, s.count - skip)};
+  uint4* const staged = data + skip;
+  slice_load(src, a.V, piece, staged, &bars[warp]);
   const double invT = a.inv_t;
   const float c = a.log2e_t;
   const float t = id >= 0 ? t_in : -INFINITY;
@@ -495,25 +497,38 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     }
     if (twice && want >= 0) flags |= SSD_ROW_BAD_TOKEN;
   }
-  flags |= slice_wait(&bar, 0);
-
-  // Take this slice's atoms out of the staged row.
-  const bool mine = id >= v0 && id < v1;
-  float z_atom = -INFINITY;
-  if (mine) {
-    TIn* at = reinterpret_cast<TIn*>(data) + (id + s.head - s.first * VE);
-    z_atom = Elem<TIn>::to_float(*at);
-    *at = Elem<TIn>::neg_inf();
+  __syncwarp();
+  if (!mbar_wait_bounded(&bars[warp], 0, kRowWaitNs)) {
+    flags |= SSD_ROW_DEVICE_TIMEOUT;
+    (void)mbar_wait_bounded(&bars[warp], 0, kRowWaitNs);  // the copies still target this CTA's shared memory
   }
+  __syncwarp();
+
+  // Take the piece's atoms out of the staged row.
+  const int w0 = max(piece.first * VE - piece.head, 0);
+  const int w1 = piece.count > 0 ? min((piece.first + piece.count) * VE - piece.head, a.V) : w0;
+#pragma unroll 1
+  for (int i = lane; i < a.M; i += 32) {
+    const int at = ids[i];
+    if (at >= w0 && at < w1) {
+      TIn* const e = reinterpret_cast<TIn*>(staged) + (at + piece.head - piece.first * VE);
+      logits[i] = Elem<TIn>::to_float(*e);
+      *e = Elem<TIn>::neg_inf();
+    }
+  }
+  __syncwarp();
+  const float m = warp_max_nan(slice_max<TIn, 32>(staged, piece.count, lane));
+  const float ref = is_number(m) ? m : 0.f;
+  float sum = slice_exp_sum<TIn, 32>(staged, piece.count, ref, c, lane);
   __syncthreads();
 
+  const bool mine = id >= v0 && id < v1;
+  const float z_atom = mine ? logits[tid] : -INFINITY;
   const double t_rel = static_cast<double>(t) * invT - teacher.top;
   const float p = ex2(static_cast<float>(t_rel * 1.4426950408889634)) * teacher.inv_total;
   {
-    const float m = warp_max_nan(slice_max<TIn>(data, s.count));
     if (!(m < INFINITY)) flags |= SSD_ROW_NONFINITE;
-    const float ref = is_number(m) ? m : 0.f;
-    float sum = warp_sum(slice_exp_sum<TIn>(data, s.count, ref, c));
+    sum = warp_sum(sum);
     float am = -INFINITY, as = 0.f;
     double num = 0.0, weight = 0.0;
     if (warp * 32 < a.M) {
