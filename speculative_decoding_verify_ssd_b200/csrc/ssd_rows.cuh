@@ -987,6 +987,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_top_kernel(const TopArgs a
       mbar_init(&bar, 1);
       mbar_init_fence();
     }
+    __syncwarp();  // the other lanes poll the barrier too
     slice_load(src, a.V, s, data, &bar);
   }
   if (tid == 0) n_pool = n_vecs = 0;

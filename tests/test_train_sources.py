@@ -1,0 +1,26 @@
+"""Properties of the training kernels' sources that a run cannot show reliably:
+what happens between the threads of a warp depends on how they are scheduled."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "speculative_decoding_verify_ssd_b200", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("name,kernels", [("ssd_rows.cuh", 2), ("ssd_linear.cuh", 1)])
+def test_barriers_are_published_before_they_are_polled(name, kernels):
+    """Between a thread's initialisation of an mbarrier and the next use of one,
+    all threads that may poll it meet at a barrier."""
+    body = source(name)
+    starts = [m.end() for m in re.finditer(r"mbar_init_fence\(\);", body)]
+    assert len(starts) == kernels
+    for at in starts:
+        use = re.search(r"\b(slice_load|slice_wait|mbar_wait_bounded|mbar_try_wait|wait)\(", body[at:])
+        assert re.search(r"__syncwarp\(\)|__syncthreads\(\)|\.sync\(\)", body[at:at + use.start()]), body[at:at + use.end()]
