@@ -30,7 +30,12 @@ constexpr int kAccCols = 256;      // TMEM columns of one accumulator
 constexpr int kBlockK = 64;        // one 128-byte swizzle row of bf16
 constexpr int kATile = 128 * kBlockK * 2;
 constexpr int kOutBuf = 32 * 128;  // one epilogue warp's staging buffer: 32 rows of 128 bytes
-constexpr unsigned long long kGemmWaitNs = 2000000000ull;
+
+// Limit of the product kernel's waits between its roles (a test build shortens it).
+#ifndef SSD_GEMM_WAIT_NS
+#define SSD_GEMM_WAIT_NS 2000000000ull
+#endif
+constexpr unsigned long long kGemmWaitNs = SSD_GEMM_WAIT_NS;
 
 enum GemmOp { kOpLse = 0, kOpGrad = 1, kOpBack = 2, kOpDh = 3, kOpDw = 4 };
 constexpr bool is_back(int op) { return op >= kOpBack; }
@@ -456,7 +461,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       const int n_valid = a.v_count - tile.n * kTileN;  // lse, grad: columns inside the vocabulary
-      if (!wait(&tfull[acc], acc_phase)) break;
+      // one decision for the warp: lanes that gave up alone would leave the others at its barriers
+      if (!__all_sync(0xFFFFFFFFu, wait(&tfull[acc], acc_phase))) break;
       tc_fence_after();
       const uint32_t src = tmem + acc * kAccCols + (static_cast<uint32_t>(quad * 32) << 16);
       float mx = -INFINITY, sum = 0.f;

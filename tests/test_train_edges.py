@@ -6,9 +6,10 @@ import math
 import pytest
 import torch
 
+from speculative_decoding_verify_ssd_b200 import _build
 from speculative_decoding_verify_ssd_b200 import binding as ssd
 
-from train_testlib import logits_like, top_ref
+from train_testlib import linear_case, linear_ref, logits_like, top_ref
 
 BF16, FP32 = torch.bfloat16, torch.float32
 
@@ -26,3 +27,46 @@ def test_top_blocks_on_used_shared_memory():
         assert (r.status == 0).all() and torch.equal(r.tokens, tokens) and torch.equal(r.values.double(), values)
         first = r if first is None else first
         assert torch.equal(r.lse, first.lse) and torch.equal(r.tail, first.tail)
+
+
+# ---------------------------------------------------------------------------
+# Waits that give up: a build whose product kernel waits 200 ns past its first
+# polls (of up to 100 us each) instead of 2 s.  The first tile of a head 65536
+# wide takes longer than that, so its epilogue gives up; the copies and products
+# that are under way still land, since a block that gave up stays 20 ms.
+# ---------------------------------------------------------------------------
+class Library:
+    """Calls of the bindings go to another build inside the `with`."""
+
+    def __init__(self, path):
+        self.path = path
+
+    def __enter__(self):
+        self.saved = _build.LIB, ssd._lib
+        _build.LIB, ssd._lib = self.path, None
+        ssd.load(build_if_missing=False)
+
+    def __exit__(self, *exc):
+        _build.LIB, ssd._lib = self.saved
+
+
+@pytest.fixture(scope="module")
+def short_wait():
+    return Library(_build.build_variant("shortgemm", ["SSD_GEMM_WAIT_NS=200ull"]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [5, 200])          # single blocks, and pairs
+def test_forward_that_gives_up_is_flagged(short_wait, N):
+    hidden, weight, targets = linear_case((N,), 65536, 700, 73)
+    targets[2] = -1
+    with short_wait:
+        r = ssd.ssd_linear_ce(hidden, weight, targets)
+        torch.cuda.synchronize()
+    on = targets >= 0
+    # (what the products left may be no number besides)
+    assert (r.status[on] & ssd.ROW_DEVICE_TIMEOUT != 0).all() and r.loss[on].isnan().all() and r.lse[on].isnan().all()
+    assert r.status[2] == 0 and r.loss[2] == 0
+    r = ssd.ssd_linear_ce(hidden, weight, targets)      # the usual limits: the answer
+    f = linear_ref(hidden, weight, targets)
+    assert (r.status == 0).all() and ((r.loss.double() - f["loss"]).abs() <= f["loss_tol"])[on].all()

@@ -24,3 +24,13 @@ def test_barriers_are_published_before_they_are_polled(name, kernels):
     for at in starts:
         use = re.search(r"\b(slice_load|slice_wait|mbar_wait_bounded|mbar_try_wait|wait)\(", body[at:])
         assert re.search(r"__syncwarp\(\)|__syncthreads\(\)|\.sync\(\)", body[at:at + use.start()]), body[at:at + use.end()]
+
+
+def test_a_warp_gives_up_as_one():
+    """A wait that a whole warp takes ends it for all lanes or for none; the
+    other waits of the product kernel are one lane's."""
+    body = source("ssd_linear.cuh")
+    kernel = body[body.index("ssd_gemm_kernel(const"):]
+    epilogue = kernel[kernel.index("const int quad"):kernel.index("ssd_linear_prep_kernel")]
+    waits = re.findall(r"[^;\n]*\bwait\(&[^;\n]*", epilogue)
+    assert len(waits) == 1 and "__all_sync(0xFFFFFFFFu, wait(" in waits[0]
