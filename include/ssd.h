@@ -407,6 +407,9 @@ size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
  *   tail, all logits -inf, or a teacher without weight), SSD_ROW_BAD_TOKEN (an
  *   id outside [-1, V) or twice in a row): loss NaN, gradient 0.
  *   SSD_ROW_ZERO_Q (informational): q is 0 where p is not; the loss is +inf.
+ *   SSD_ROW_DEVICE_TIMEOUT (an error of the GPU: a wait gave up after 1 s and
+ *   more): loss NaN, gradient 0, or NaN in the places of a thread block that
+ *   gave up by itself, whether or not the status tells.
  */
 ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_batch, int V,
                        int64_t batch_stride, int64_t row_stride, float T, int M, const int32_t* tokens,

@@ -361,7 +361,7 @@ struct DistillJoin {
   GradScale scale;       // outside the atoms; k 0: none, or a void row
   float at_top, weight;  // on an atom: weight * (2^((z - at_top) c) / total - p)
   float total;
-  int bad, far;
+  int bad, far, late;
 };
 
 struct DistillArgs {
@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
   bool bad = false;
   int late = 0;
   if (warp == 0) {
-    late = parts_wait(&parts_bar);
+    // one verdict for the warp: a part that only some lanes waited long enough for counts for none
+    late = static_cast<int>(__reduce_or_sync(0xFFFFFFFFu, static_cast<unsigned>(parts_wait(&parts_bar))));
     if (lane < C) q = *reinterpret_cast<const float4*>(&parts[lane]);
     tail_max = warp_max_nan(q.x);
     atom_max = warp_max_nan(q.z);
@@ -593,7 +594,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
       const float k = bad || !(tail > 0.f) ? 0.f : w * (tail_share / total - teacher.p_tail) / tail;
       const float ref = tail > 0.f ? tail_max : 0.f;
       const bool far = !(fabsf(ref * c) <= 1024.f);
-      join = DistillJoin{{k, log2f(fabsf(k)) - (far ? 0.f : ref * c), ref, c}, at_top, w, total, bad, far};
+      join = DistillJoin{{k, log2f(fabsf(k)) - (far ? 0.f : ref * c), ref, c}, at_top, w, total, bad, far, late};
     }
   }
   if (dst) {
@@ -622,9 +623,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
         for (int i = tid; i < s.count; i += kRowThreads) by_element(i, value(i));
       }
     };
-    if (j.scale.k == 0.f)  // also a void row, whose logits may be NaN
-      write([](int) { return make_uint4(0u, 0u, 0u, 0u); });
-    else if (sizeof(TIn) == 2 && j.far)
+    if (j.scale.k == 0.f) {  // also a void row, whose logits may be NaN
+      // NaN (in either type) where only this CTA gave up: the first one's status need not tell
+      const uint32_t w = j.late ? 0x7FC07FC0u : 0u;
+      write([w](int) { return make_uint4(w, w, w, w); });
+    } else if (sizeof(TIn) == 2 && j.far)
       j.scale.k < 0.f ? write([&](int i) { return gradient_of<TIn, true, true>(data[i], j.scale); })
                       : write([&](int i) { return gradient_of<TIn, false, true>(data[i], j.scale); });
     else if (sizeof(TIn) == 2 && j.scale.k < 0.f)

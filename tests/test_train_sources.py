@@ -34,3 +34,13 @@ def test_a_warp_gives_up_as_one():
     epilogue = kernel[kernel.index("const int quad"):kernel.index("ssd_linear_prep_kernel")]
     waits = re.findall(r"[^;\n]*\bwait\(&[^;\n]*", epilogue)
     assert len(waits) == 1 and "__all_sync(0xFFFFFFFFu, wait(" in waits[0]
+
+
+def test_a_cluster_part_is_late_for_a_warp_as_one():
+    """All lanes of the joining warp share one verdict on the cluster's parts,
+    and a block that gave up alone leaves NaN, not zeros, in its slice."""
+    body = source("ssd_rows.cuh")
+    kernel = body[body.index("ssd_distill_kernel(const"):]
+    waits = re.findall(r"[^;\n]*\bparts_wait\(&[^;\n]*", kernel)
+    assert len(waits) == 1 and "__reduce_or_sync(0xFFFFFFFFu" in waits[0]
+    assert re.search(r"j\.late \? 0x7FC07FC0u : 0u", kernel)
