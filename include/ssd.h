@@ -429,7 +429,8 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
  *   lse 0; its hidden state is not read), so ssd_verify's out_tokens, -1 behind
  *   the bonus, are targets as they are.  loss, lse, status [N] out:
  *   SSD_ROW_BAD_TOKEN (target >= V), SSD_ROW_NONFINITE (NaN or infinite
- *   logits): loss and lse NaN.
+ *   logits), SSD_ROW_DEVICE_TIMEOUT (an error of the GPU: a wait gave up):
+ *   loss and lse NaN.
  *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 0) bytes, 256-byte
  *   aligned; it needs no initial contents, and calls that overlap on the GPU
  *   must not share one.  Results are the same bits on every call.
@@ -451,7 +452,9 @@ ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int 
  *   16-byte aligned; every element is written.  Rows with a negative target or
  *   row_scale 0 have no part and grad_hidden 0, nor have rows with a target
  *   >= V or an lse that is not finite.  status [N] out, or NULL: those last
- *   two, as ssd_linear_ce names them.
+ *   two, as ssd_linear_ce names them, and SSD_ROW_DEVICE_TIMEOUT on all rows
+ *   that take part where a wait gave up (an error of the GPU); grad_weight and
+ *   those rows of grad_hidden are then NaN.
  *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 1) bytes, otherwise as in
  *   ssd_linear_ce.
  */

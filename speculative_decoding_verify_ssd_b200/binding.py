@@ -726,12 +726,25 @@ def ssd_linear_ce(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Ten
     return _launch(dev.index, stream, call)
 
 
+class LinearCeGrads(tuple):
+    """(grad_hidden, grad_weight), with the rows' status as an attribute."""
+
+    def __new__(cls, grad_hidden, grad_weight, status):
+        self = super().__new__(cls, (grad_hidden, grad_weight))
+        self.status = status
+        return self
+
+    grad_hidden = property(lambda self: self[0])
+    grad_weight = property(lambda self: self[1])
+
+
 def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
                        row_scale: Optional[torch.Tensor] = None, grad_hidden: Optional[torch.Tensor] = None,
                        grad_weight: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                       workspace: Optional[torch.Tensor] = None, stream=None):
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> LinearCeGrads:
     """(grad_hidden, grad_weight) of sum(row_scale * loss), loss and lse being
-    ssd_linear_ce's (see ssd_linear_ce_grad in ssd.h)."""
+    ssd_linear_ce's (see ssd_linear_ce_grad in ssd.h); the pair's `status` holds
+    the rows' status bits."""
     dev, lead, N, D, V, args = _linear_args(hidden, weight, targets)
     index = dev.index
     _want(lse, "lse", torch.float32, lead, index)
@@ -751,8 +764,9 @@ def ssd_linear_ce_grad(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
             gh = torch.empty_like(hidden, memory_format=torch.contiguous_format)
         if gw is None:
             gw = torch.empty_like(weight, memory_format=torch.contiguous_format)
+        st_rows = torch.empty_like(targets) if status is None else status
         _check(load().ssd_linear_ce_grad(*args, lse.data_ptr(), _ptr(row_scale), gh.data_ptr(), gw.data_ptr(),
-                                         _ptr(status), ws.data_ptr(), ws.numel(), st), "ssd_linear_ce_grad")
-        return gh, gw
+                                         st_rows.data_ptr(), ws.data_ptr(), ws.numel(), st), "ssd_linear_ce_grad")
+        return LinearCeGrads(gh, gw, st_rows)
 
     return _launch(index, stream, call)

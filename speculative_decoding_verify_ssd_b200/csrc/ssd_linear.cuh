@@ -802,14 +802,22 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 constexpr int kDhThreads = 128;
 
-// Sums dh's slots in order, scales and rounds once, and puts the rows in their places.
+// Sums dh's slots in order, scales and rounds once, and puts the rows in their
+// places.  After a wait that gave up, both gradients are NaN: parts of the
+// weight's may be unwritten, and it has no status of its own.
 __global__ void __launch_bounds__(kDhThreads)
     ssd_linear_dh_kernel(const LinearHdr* hdr, const float* part, int rows, int slots, int D, const int32_t* index,
-                         uint16_t* grad_hidden, int32_t* status) {
+                         uint16_t* grad_hidden, uint4* grad_weight, size_t weight_vecs, int32_t* status) {
   const int r = static_cast<int>(blockIdx.x);
   const int d = (static_cast<int>(blockIdx.y) * kDhThreads + static_cast<int>(threadIdx.x)) * 4;
   stream_wait();
   const LinearHdr h = *hdr;
+  if (h.error) {
+    const size_t step = static_cast<size_t>(gridDim.x) * gridDim.y * kDhThreads;
+    for (size_t i = (static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kDhThreads + threadIdx.x;
+         i < weight_vecs; i += step)
+      grad_weight[i] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+  }
   if (r >= h.n_active || d >= D) return;
   const int n = index[r];
   if (h.error && status && d == 0) status[n] = SSD_ROW_DEVICE_TIMEOUT;

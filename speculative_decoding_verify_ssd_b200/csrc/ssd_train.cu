@@ -365,7 +365,8 @@ static ssd_status linear_backward(const LinearPlan& p, char* ws, const void* wei
   const dim3 grid(static_cast<unsigned>(N), static_cast<unsigned>((D / 4 + kDhThreads - 1) / kDhThreads));
   return launch_dependent(&ssd_linear_dh_kernel, grid, kDhThreads, 0, 0, stream, g.hdr,
                           reinterpret_cast<const float*>(ws + p.dh), p.rows, p.slots, D,
-                          reinterpret_cast<const int32_t*>(ws + p.index), static_cast<uint16_t*>(grad_hidden), status);
+                          reinterpret_cast<const int32_t*>(ws + p.index), static_cast<uint16_t*>(grad_hidden),
+                          static_cast<uint4*>(grad_weight), static_cast<size_t>(V) * D / 8, status);
 }
 
 }  // namespace ssd

@@ -70,3 +70,40 @@ def test_forward_that_gives_up_is_flagged(short_wait, N):
     r = ssd.ssd_linear_ce(hidden, weight, targets)      # the usual limits: the answer
     f = linear_ref(hidden, weight, targets)
     assert (r.status == 0).all() and ((r.loss.double() - f["loss"]).abs() <= f["loss_tol"])[on].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [5, 200])
+def test_gradient_that_gives_up_is_flagged(short_wait, N):
+    """Neither gradient holds a number, with or without a status array."""
+    hidden, weight, targets = linear_case((N,), 65536, 700, 74)
+    targets[2] = -1
+    on = targets >= 0
+    r = ssd.ssd_linear_ce(hidden, weight, targets)
+    with short_wait:
+        given = torch.full_like(targets, 77)
+        outs = [ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse),
+                ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse, status=given)]
+        torch.cuda.synchronize()
+    assert outs[1].status is given
+    for g in outs:
+        assert g.grad_weight.isnan().all() and g.grad_hidden[on].isnan().all() and (g.grad_hidden[2] == 0).all()
+        assert (g.status[on] == ssd.ROW_DEVICE_TIMEOUT).all() and g.status[2] == 0
+    dh, dw = g = ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse)
+    f = linear_ref(hidden, weight, targets)
+    assert (g.status == 0).all()
+    assert ((dh.double() - f["dh"]).abs() <= f["dh_tol"]).all()
+    assert ((dw.double() - f["dw"]).abs() <= f["dw_tol"]).all()
+
+
+@pytest.mark.gpu
+def test_gradient_status_without_being_asked():
+    hidden, weight, targets = linear_case((9,), 64, 50, 75)
+    targets[4] = 50
+    r = ssd.ssd_linear_ce(hidden, weight, targets)
+    r.lse[7] = math.inf
+    g = ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse)
+    want = torch.zeros(9, dtype=torch.int32, device="cuda")
+    want[4], want[7] = ssd.ROW_BAD_TOKEN, ssd.ROW_NONFINITE
+    assert isinstance(g, tuple) and len(g) == 2 and g[0] is g.grad_hidden and g[1] is g.grad_weight
+    assert torch.equal(g.status, want)
