@@ -380,7 +380,8 @@ ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_
                            float* values, float* lse, float* tail, int32_t* status, void* workspace,
                            size_t ws_bytes, void* stream);
 
-/* Workspace size of ssd_teacher_top for `rows` rows in all; 0 where it needs
+/* Workspace size of ssd_teacher_top for `rows` rows in all, or any smaller
+ * number of them (one workspace serves a shrinking batch); 0 where it needs
  * none (workspace may then be NULL) and for invalid sizes. */
 size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
 
@@ -465,7 +466,7 @@ ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype,
                               void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace size of ssd_linear_ce (grad 0) and ssd_linear_ce_grad (grad 1) at
- * N rows; 0 for invalid sizes. */
+ * N rows or any smaller number of them; 0 for invalid sizes. */
 size_t ssd_linear_ce_workspace_bytes(int N, int D, int V, int grad);
 
 /* Workspace size in bytes for ssd_verify / ssd_saguaro_reweight at

@@ -124,6 +124,18 @@ static bool top_plan(long long rows, int V, int esize, TopPlan* p) {
   return true;
 }
 
+// Workspace that serves `rows` rows and every smaller number of them: few rows
+// are cut into more slices, so a plan's own need is not monotone.  From kRowFill
+// rows on the slices of a row no longer depend on their number.
+static size_t top_workspace(long long rows, int V, int esize) {
+  TopPlan p;
+  if (!top_plan(rows, V, esize, &p)) return 0;
+  size_t most = p.total;
+  for (long long r = 1; r < rows && r <= kRowFill; ++r)
+    if (top_plan(r, V, esize, &p) && p.total > most) most = p.total;
+  return most;
+}
+
 // Checks common to the row calls.
 static ssd_status check_rows(int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,
                              int64_t row_stride, float T, int M) {
@@ -245,6 +257,18 @@ static LinearPlan linear_plan(int N, int D, int V, bool grad) {
   }
   p.total = off;
   return p;
+}
+
+// Workspace that serves N rows and every smaller number of them: splits and
+// pieces jump with the row tiles, so a plan's own need is not monotone.  A plan
+// changes at multiples of kBlockK rows only.
+static size_t linear_workspace(int N, int D, int V, bool grad) {
+  size_t most = linear_plan(N, D, V, grad).total;
+  for (int n = kBlockK; n < N; n += kBlockK) {
+    const size_t need = linear_plan(n, D, V, grad).total;
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 template <int Op, int CG>
@@ -376,9 +400,8 @@ using namespace ssd;
 extern "C" {
 
 size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M) {
-  TopPlan p;
   if (check_rows(dtype, 1, rows, V, 0, 0, 1.f, M) != SSD_OK || rows == 0) return 0;
-  return top_plan(rows, V, dtype == SSD_DTYPE_FP32 ? 4 : 2, &p) ? p.total : 0;
+  return top_workspace(rows, V, dtype == SSD_DTYPE_FP32 ? 4 : 2);
 }
 
 ssd_status ssd_teacher_top(const void* logits, int dtype, int n_batch, int rows_per_batch, int V, int64_t batch_stride,
@@ -462,7 +485,7 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
 size_t ssd_linear_ce_workspace_bytes(int N, int D, int V, int grad) {
   if (N < 0 || N > SSD_MAX_LINEAR_N || D < 8 || D % 8 != 0 || D > SSD_MAX_LINEAR_D || V < 1 || V > SSD_MAX_LINEAR_V)
     return 0;
-  return linear_plan(N > 0 ? N : 1, D, V, grad != 0).total;
+  return linear_workspace(N > 0 ? N : 1, D, V, grad != 0);
 }
 
 ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int n_batch, int rows_per_batch, int D,

@@ -14,6 +14,47 @@ from train_testlib import linear_case, linear_ref, logits_like, top_ref
 BF16, FP32 = torch.bfloat16, torch.float32
 
 
+# ---------------------------------------------------------------------------
+# Workspaces.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("V,dtype", [(128256, 1), (151936, 1), (151936, 0), (32003, 0), (70001, 1), (400000, 0)])
+def test_top_workspace_serves_fewer_rows(V, dtype):
+    L = ssd.load()
+    sizes = [L.ssd_teacher_top_workspace_bytes(n, V, dtype, 8) for n in range(1, 1200)]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("D,V", [(8, 300), (64, 5003), (256, 20011), (1024, 32000), (2048, 128256), (64, 60001)])
+@pytest.mark.parametrize("grad", [0, 1])
+def test_linear_workspace_serves_fewer_rows(D, V, grad):
+    L = ssd.load()
+    sizes = [L.ssd_linear_ce_workspace_bytes(n, D, V, grad) for n in list(range(1, 2200)) + [5000, 70000, 1 << 18]]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_a_shrinking_batch():
+    """Sized for the largest batch, dirty, used at sizes whose own plans need more than a larger one's."""
+    V = 128256
+    z = logits_like((64,), V, BF16, 76)
+    ws = torch.empty(ssd.teacher_top_workspace_bytes(64, V, ssd.DTYPE_BF16, 16), dtype=torch.uint8, device="cuda")
+    tokens, values, _, _ = top_ref(z, 16, 1.0)
+    for n in (64, 59, 42, 29, 19, 1):
+        ws.fill_(255)
+        r = ssd.ssd_teacher_top(z[:n], 16, workspace=ws)
+        assert (r.status == 0).all() and torch.equal(r.tokens, tokens[:n]) and torch.equal(r.values.double(), values[:n])
+    hidden, weight, targets = linear_case((1030,), 256, 20011, 77)
+    ws = torch.empty(ssd.linear_ce_workspace_bytes(1030, 256, 20011, True), dtype=torch.uint8, device="cuda")
+    for n in (1030, 960, 640, 129, 3):
+        h, y = hidden[:n], targets[:n]
+        ws.fill_(255)
+        r = ssd.ssd_linear_ce(h, weight, y, workspace=ws)
+        ws.fill_(255)
+        dh, dw = ssd.ssd_linear_ce_grad(h, weight, y, r.lse, workspace=ws)
+        dh2, dw2 = ssd.ssd_linear_ce_grad(h, weight, y, r.lse)
+        assert (r.status == 0).all() and torch.equal(dh, dh2) and torch.equal(dw, dw2)
+
+
 @pytest.mark.gpu
 def test_top_blocks_on_used_shared_memory():
     """Thousands of blocks one after the other on shared memory (their barriers'
