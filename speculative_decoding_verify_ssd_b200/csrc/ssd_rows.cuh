@@ -822,7 +822,8 @@ __device__ __forceinline__ void top_logs(const TopArgs& a, int row, float row_ma
   if (lane == 1) a.lse[row] = static_cast<float>(static_cast<double>(row_max) * a.inv_t + logs);
 }
 
-constexpr int kMaxTopSlices = 16;
+constexpr int kTopSlices = 16;     // slices of a row, as far as they hold it
+constexpr int kMaxTopSlices = 32;  // of a row of more than 3.2 MB
 constexpr int kShort = 512;  // keys of a row that are ranked from a list of their own (even)
 
 // Shared memory of top_finish.

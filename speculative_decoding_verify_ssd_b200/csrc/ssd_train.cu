@@ -110,9 +110,11 @@ static bool top_plan(long long rows, int V, int esize, TopPlan* p) {
   // against 18.5, 384 of 62 KB 16.5 against 23.9; but 384 of 195 KB 43 against
   // 33 (and 97 KB the same).
   if (bytes <= kRowOne || (rows <= kSmCount && bytes <= kSliceMax)) n = 1;
-  if (n > kMaxTopSlices) n = kMaxTopSlices;
+  if (n > kTopSlices) n = kTopSlices;
+  const long long need = (bytes + kSliceMax - 1) / kSliceMax;
+  if (n < need) n = need;
+  if (n > kMaxTopSlices || rows * n > 0x7FFFFFFFLL) return false;
   const long long sv = (vecs + n - 1) / n;
-  if (sv * 16 > kSliceMax || rows * n > 0x7FFFFFFFLL) return false;
   p->slices = static_cast<int>(n);
   p->slice_vecs = static_cast<int>(sv);
   p->smem = static_cast<int>(n > 1 || sv * 16 > static_cast<long long>(sizeof(TopFinish)) ? sv * 16 : sizeof(TopFinish));

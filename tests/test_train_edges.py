@@ -9,6 +9,7 @@ import torch
 from speculative_decoding_verify_ssd_b200 import _build
 from speculative_decoding_verify_ssd_b200 import binding as ssd
 
+from test_train_rows import check_distill, check_top, teacher
 from train_testlib import linear_case, linear_ref, logits_like, top_ref
 
 BF16, FP32 = torch.bfloat16, torch.float32
@@ -68,6 +69,34 @@ def test_top_blocks_on_used_shared_memory():
         assert (r.status == 0).all() and torch.equal(r.tokens, tokens) and torch.equal(r.values.double(), values)
         first = r if first is None else first
         assert torch.equal(r.lse, first.lse) and torch.equal(r.tail, first.tail)
+
+
+# ---------------------------------------------------------------------------
+# Limits.
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("V,dtype", [(819197, 0), (1600000, 0), (1638393, 1), (3200000, 1)])
+def test_longest_top_rows_have_a_workspace(V, dtype):
+    L = ssd.load()
+    assert L.ssd_teacher_top_workspace_bytes(1, V, dtype, 8) > 0
+    assert L.ssd_teacher_top_workspace_bytes(1, 3300001 // (2 if dtype == 0 else 1), dtype, 8) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(819195, FP32), (819201, FP32), (1600000, FP32), (1638389, BF16), (3200000, BF16)])
+def test_longest_top_rows(V, dtype):
+    """16 slices of 200 KB, and more of them up to the documented 6.4 MB; at odd places too."""
+    z = logits_like((2,), V + 1, dtype, 78)
+    check_top(z[:, 1:], 256, 0.8)
+    check_top(z[:, :V], 7, 1.0)
+    check_top((z[:, :V] * 2).round(), 200, 1.0)     # slices full of equal logits
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(400000, FP32), (800000, BF16)])
+def test_longest_distill_rows(V, dtype):
+    z = logits_like((2,), V + 1, dtype, 79)[:, 1:]
+    tokens, values, tail = teacher((2,), V, 100, 1.0, 80, True)
+    check_distill(z, tokens, values, tail, 1.0)
 
 
 # ---------------------------------------------------------------------------
