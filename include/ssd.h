@@ -399,7 +399,8 @@ size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
  *   1 <= M <= min(V, SSD_MAX_TOP).  tokens [rows, M]: distinct ids, in any
  *   order, -1 for an absent atom; values [rows, M] (-inf: no weight); tail [rows] or NULL.  row_scale [rows] or NULL (1): the
  *   factor of the row's gradient (loss is not scaled).  A row of row_scale 0
- *   is left out: its logits and teacher are not read, loss 0, gradient 0.
+ *   is left out: its logits and teacher are not read, loss 0, gradient 0.  One
+ *   that is not finite makes the row's own gradient so.
  *   loss [rows], status [rows] out.  grad: NULL, or the gradient with respect
  *   to the logits, in their dtype, [n_batch, rows_per_batch, V] with its own
  *   strides; it may be the logits themselves (same pointer and strides), and
@@ -452,8 +453,8 @@ ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int 
  *   (1).  grad_hidden [N, D] out, grad_weight [V, D] out, bf16, dense,
  *   16-byte aligned; every element is written.  Rows with a negative target or
  *   row_scale 0 have no part and grad_hidden 0, nor have rows with a target
- *   >= V or an lse that is not finite.  status [N] out, or NULL: those last
- *   two, as ssd_linear_ce names them, and SSD_ROW_DEVICE_TIMEOUT on all rows
+ *   >= V (SSD_ROW_BAD_TOKEN) or an lse or row_scale that is not finite
+ *   (SSD_ROW_NONFINITE).  status [N] out, or NULL: those two, and SSD_ROW_DEVICE_TIMEOUT on all rows
  *   that take part where a wait gave up (an error of the GPU); grad_weight and
  *   those rows of grad_hidden are then NaN.
  *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 1) bytes, otherwise as in

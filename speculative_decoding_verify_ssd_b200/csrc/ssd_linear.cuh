@@ -625,8 +625,8 @@ struct PrepArgs {
 };
 
 // Whether row n takes part, and its status where it does not.  A row whose
-// log-normaliser is not finite is left out of the gradient: its NaN would reach
-// every row of the weight's gradient.
+// log-normaliser or scale is not finite is left out of the gradient: its NaN
+// would reach every row of the weight's gradient.
 __device__ __forceinline__ bool row_active(const PrepArgs& a, int n, int32_t* status) {
   const int t = a.targets[n];
   *status = 0;
@@ -636,7 +636,7 @@ __device__ __forceinline__ bool row_active(const PrepArgs& a, int n, int32_t* st
     *status = SSD_ROW_BAD_TOKEN;
     return false;
   }
-  if (a.lse && !(fabsf(a.lse[n]) < INFINITY)) {
+  if ((a.lse && !(fabsf(a.lse[n]) < INFINITY)) || (a.row_scale && !(fabsf(a.row_scale[n]) < INFINITY))) {
     *status = SSD_ROW_NONFINITE;
     return false;
   }

@@ -100,6 +100,45 @@ def test_longest_distill_rows(V, dtype):
 
 
 # ---------------------------------------------------------------------------
+# Scales and logits that are not finite.
+# ---------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [7, 300])
+def test_linear_scales_that_are_not_finite(N):
+    """Such a row is flagged and left out; the others' gradients are as if it were not there."""
+    hidden, weight, targets = linear_case((N,), 72, 500, 81)
+    scale = torch.rand(N, device="cuda") + 0.5
+    for i, bad in ((1, math.nan), (3, math.inf), (6, -math.inf)):
+        scale[i] = bad
+    targets[0], targets[6] = 500, -1
+    r = ssd.ssd_linear_ce(hidden, weight, targets)
+    g = ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse, row_scale=scale)
+    want = torch.zeros(N, dtype=torch.int32, device="cuda")
+    want[0], want[1], want[3] = ssd.ROW_BAD_TOKEN, ssd.ROW_NONFINITE, ssd.ROW_NONFINITE
+    assert torch.equal(g.status, want)
+    only, without = targets.clone(), scale.clone()
+    only[[0, 1, 3]] = -1
+    without[[0, 1, 3, 6]] = 0
+    f = linear_ref(hidden, weight, only, without)
+    assert (g.grad_hidden[[0, 1, 3, 6]] == 0).all()
+    assert ((g.grad_hidden.double() - f["dh"]).abs() <= f["dh_tol"]).all()
+    assert ((g.grad_weight.double() - f["dw"]).abs() <= f["dw_tol"]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_distill_scales_that_are_not_finite(dtype):
+    z = logits_like((4,), 700, dtype, 82)
+    tokens, values, tail = teacher((4,), 700, 9, 1.0, 83, True)
+    scale = torch.tensor([1.0, math.nan, math.inf, 2.0], device="cuda")
+    r = ssd.ssd_distill(z, tokens, values, tail, row_scale=scale)
+    e = ssd.ssd_distill(z, tokens, values, tail, row_scale=torch.ones_like(scale) + (scale == 2.0))
+    assert (r.status == 0).all() and torch.equal(r.loss, e.loss)
+    assert not r.grad[1:3].isfinite().any()
+    assert torch.equal(r.grad[[0, 3]], e.grad[[0, 3]])
+
+
+# ---------------------------------------------------------------------------
 # Waits that give up: a build whose product kernel waits 200 ns past its first
 # polls (of up to 100 us each) instead of 2 s.  The first tile of a head 65536
 # wide takes longer than that, so its epilogue gives up; the copies and products
