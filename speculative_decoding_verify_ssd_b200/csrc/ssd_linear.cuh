@@ -621,8 +621,9 @@ struct PrepArgs {
   uint16_t* grad_hidden;   // gradient call: likewise
   int32_t* status;         // may be NULL in the gradient call
   int N, V, D;
-  int block_rows;          // rows of one block, at most 32
+  int block_rows;          // rows of one block, at most kPrepRows
 };
+constexpr int kPrepRows = 256;
 
 // Whether row n takes part, and its status where it does not.  A row whose
 // log-normaliser or scale is not finite is left out of the gradient: its NaN
@@ -646,7 +647,7 @@ __device__ __forceinline__ bool row_active(const PrepArgs& a, int n, int32_t* st
 __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const PrepArgs a) {
   __shared__ int ired[kRowWarps];
   __shared__ float fred[kRowWarps];
-  __shared__ int place[32];
+  __shared__ int place[kPrepRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n0 = static_cast<int>(blockIdx.x) * a.block_rows;
   stream_wait();
@@ -669,13 +670,14 @@ __global__ void __launch_bounds__(kRowThreads) ssd_linear_prep_kernel(const Prep
     if (!(top > 0.f && top < INFINITY)) top = 1.f;
   }
   if (blockIdx.x == 0 && tid == 0) *a.hdr = LinearHdr{total, 0, top};
-  if (warp == 0) {
-    const int n = n0 + lane;
-    const bool in = lane < a.block_rows && n < a.N;
+  for (int i0 = 0; warp == 0 && i0 < a.block_rows; i0 += 32) {
+    const int i = i0 + lane, n = n0 + i;
+    const bool in = i < a.block_rows && n < a.N;
     const bool on = in && row_active(a, n, &st);
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, on);
     const int at = before + __popc(mask & ((1u << lane) - 1u));
-    place[lane] = on ? at : -1;
+    before += __popc(mask);
+    if (in) place[i] = on ? at : -1;
     if (on) {
       a.index[at] = n;
       a.target[at] = a.targets[n];

@@ -308,10 +308,11 @@ static void prep_args(PrepArgs* a, const LinearPlan& p, char* ws, const RowsIn& 
 }
 
 // Few rows per block, so that the copies spread over the GPU; every block
-// reads all targets, so no more than about a thousand blocks.
+// reads all targets, so no more than 1024 blocks.
 static ssd_status launch_prep(PrepArgs& a, cudaStream_t stream) {
+  static_assert(SSD_MAX_LINEAR_N <= 1024 * kPrepRows, "a block's rows");
   int rows = (a.N + 1023) / 1024;
-  rows = rows < kRowWarps ? kRowWarps : (rows > 32 ? 32 : rows);
+  if (rows < kRowWarps) rows = kRowWarps;
   a.block_rows = rows;
   const int blocks = (a.N + rows - 1) / rows;
   const int zero = a.grad_hidden ? kBlockK / kRowWarps : 1;  // blocks that clear the rows behind the last

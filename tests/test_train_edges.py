@@ -2,6 +2,8 @@
 workspaces that earlier work left full, limits of sizes, scales and logits that
 are not finite, waits that give up."""
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -9,10 +11,12 @@ import torch
 from speculative_decoding_verify_ssd_b200 import _build
 from speculative_decoding_verify_ssd_b200 import binding as ssd
 
+from test_train_linear import check as check_linear
 from test_train_rows import check_distill, check_top, teacher
 from train_testlib import linear_case, linear_ref, logits_like, top_ref
 
 BF16, FP32 = torch.bfloat16, torch.float32
+TRAIN_CU = os.path.join(_build.CSRC, "ssd_train.cu")
 
 
 # ---------------------------------------------------------------------------
@@ -97,6 +101,23 @@ def test_longest_distill_rows(V, dtype):
     z = logits_like((2,), V + 1, dtype, 79)[:, 1:]
     tokens, values, tail = teacher((2,), V, 100, 1.0, 80, True)
     check_distill(z, tokens, values, tail, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [32768, 32769, 70001, 1 << 18])
+def test_many_head_rows(N):
+    """More rows than 1024 blocks of 32 hold, some of them left out, up to the limit."""
+    hidden, weight, targets = linear_case((N,), 16, 70, 84, keep=0.7)
+    check_linear(hidden, weight, targets, torch.rand(N, device="cuda") + 0.5)
+
+
+@pytest.mark.parametrize("N", [1, 8192, 8193, 32769, 1 << 18])
+def test_no_more_than_1024_blocks_read_all_targets(N):
+    """The gather's blocks, each of which scans the N targets (its rule, from the source)."""
+    rule = re.search(r"launch_prep\(PrepArgs& a.*?\n\}", open(TRAIN_CU).read(), re.S).group(0)
+    rows = (N + 1023) // 1024
+    assert "rows > 32" not in rule and "(a.N + 1023) / 1024" in rule
+    assert -(-N // max(rows, 8)) <= 1024 and rows <= 256
 
 
 # ---------------------------------------------------------------------------
