@@ -430,9 +430,10 @@ ssd_status ssd_distill(const void* logits, int dtype, int n_batch, int rows_per_
  *   summed in fp32.  targets [N]: a negative one leaves the row out (loss and
  *   lse 0; its hidden state is not read), so ssd_verify's out_tokens, -1 behind
  *   the bonus, are targets as they are.  loss, lse, status [N] out:
- *   SSD_ROW_BAD_TOKEN (target >= V), SSD_ROW_NONFINITE (NaN or infinite
- *   logits), SSD_ROW_DEVICE_TIMEOUT (an error of the GPU: a wait gave up):
- *   loss and lse NaN.
+ *   SSD_ROW_BAD_TOKEN (target >= V), SSD_ROW_NONFINITE (a NaN or +inf logit,
+ *   -inf at the target, or all logits -inf; elsewhere -inf is a token of no
+ *   mass), SSD_ROW_DEVICE_TIMEOUT (an error of the GPU: a wait gave up): loss
+ *   and lse NaN.
  *   workspace: ssd_linear_ce_workspace_bytes(N, D, V, 0) bytes, 256-byte
  *   aligned; it needs no initial contents, and calls that overlap on the GPU
  *   must not share one.  Results are the same bits on every call.

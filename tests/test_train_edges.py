@@ -147,6 +147,38 @@ def test_linear_scales_that_are_not_finite(N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [6, 200])
+def test_linear_logits_that_are_infinite(N):
+    """-inf is a token of no mass, except at the target; +inf and NaN void the row."""
+    hidden, weight, targets = linear_case((N,), 64, 300, 85)
+    targets[targets == 17] = 18
+    hidden[:, 0] = hidden[:, 0].abs() + 0.5
+    hidden[1, 0], hidden[2, 0], targets[3] = -1.0, 0.0, 17     # +inf, NaN, -inf at the target
+    masked = weight.clone()
+    masked[17, 0] = -math.inf
+    r = ssd.ssd_linear_ce(hidden, masked, targets)
+    void = torch.zeros(N, dtype=torch.bool, device="cuda")
+    void[1:4] = True
+    assert torch.equal(r.status, torch.where(void, ssd.ROW_NONFINITE, 0).int())
+    assert r.loss[void].isnan().all() and r.lse[void].isnan().all()
+    keep = torch.arange(300, device="cuda") != 17
+    small = torch.where(void, torch.full_like(targets, -1), targets - (targets > 17).int())
+    f = linear_ref(hidden, weight[keep], small)
+    assert ((r.loss.double() - f["loss"]).abs() <= f["loss_tol"])[~void].all()
+    g = ssd.ssd_linear_ce_grad(hidden, masked, targets, r.lse)
+    assert torch.equal(g.status, r.status)
+    assert ((g.grad_weight[keep].double() - f["dw"]).abs() <= f["dw_tol"]).all() and (g.grad_weight[17] == 0).all()
+    assert (g.grad_hidden[void] == 0).all()
+    # (in the masked column G weight is 0 * -inf)
+    d = (g.grad_hidden[:, 1:].double() - f["dh"][:, 1:]).abs()
+    assert (d <= f["dh_tol"][:, 1:])[~void].all() and g.grad_hidden[~void, 0].isnan().all()
+    none = weight.clone()
+    none[:, 0] = -math.inf                                     # every logit -inf
+    r = ssd.ssd_linear_ce(hidden[4:], none, targets[4:])
+    assert (r.status == ssd.ROW_NONFINITE).all() and r.loss.isnan().all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_distill_scales_that_are_not_finite(dtype):
     z = logits_like((4,), 700, dtype, 82)
