@@ -452,7 +452,9 @@ ssd_status ssd_linear_ce(const void* hidden, const void* weight, int dtype, int 
  *   which are summed in fp32 and rounded once.  hidden, weight, targets and
  *   strides as in ssd_linear_ce, lse [N] as it wrote it; row_scale [N] or NULL
  *   (1).  grad_hidden [N, D] out, grad_weight [V, D] out, bf16, dense,
- *   16-byte aligned; every element is written.  Rows with a negative target or
+ *   16-byte aligned; every element is written.  They overlap neither the weight
+ *   nor each other, and grad_hidden no hidden state, unless it is a dense hidden
+ *   itself.  Rows with a negative target or
  *   row_scale 0 have no part and grad_hidden 0, nor have rows with a target
  *   >= V (SSD_ROW_BAD_TOKEN) or an lse or row_scale that is not finite
  *   (SSD_ROW_NONFINITE).  status [N] out, or NULL: those two, and SSD_ROW_DEVICE_TIMEOUT on all rows

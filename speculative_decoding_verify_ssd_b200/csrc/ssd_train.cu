@@ -293,6 +293,14 @@ static ssd_status check_linear(int dtype, int n_batch, int rows_per_batch, int D
   return SSD_OK;
 }
 
+// Whether a dense block shares a byte with rows of `len` bytes, `step` apart.
+static bool overlaps(const void* block, size_t bytes, const void* base, long long rows, long long len, long long step) {
+  const long long p = static_cast<long long>(reinterpret_cast<intptr_t>(block)),
+                  b = static_cast<long long>(reinterpret_cast<intptr_t>(base));
+  const long long r = p < b + len ? 0 : (step > 0 ? (p - b - len) / step + 1 : rows);  // the first row that ends behind p
+  return r < rows && b + r * step < p + static_cast<long long>(bytes);
+}
+
 static void prep_args(PrepArgs* a, const LinearPlan& p, char* ws, const RowsIn& hidden, const int32_t* targets, int N,
                       int V, int D) {
   *a = PrepArgs{};
@@ -533,6 +541,20 @@ ssd_status ssd_linear_ce_grad(const void* hidden, const void* weight, int dtype,
     return SSD_ERR_ALIGNMENT;
   const LinearPlan p = linear_plan(N, D, V, true);
   if (!workspace || ws_bytes < p.total) return SSD_ERR_WORKSPACE;
+  // The weight is read to the end, other rows' hidden states while rows that are left out get their zeros.
+  const size_t gh_bytes = 2ull * static_cast<size_t>(N) * D, gw_bytes = 2ull * static_cast<size_t>(V) * D;
+  if (overlaps(grad_weight, gw_bytes, weight, V, 2ll * D, 2 * weight_stride) ||
+      overlaps(grad_hidden, gh_bytes, weight, V, 2ll * D, 2 * weight_stride) ||
+      overlaps(grad_hidden, gh_bytes, grad_weight, 1, static_cast<long long>(gw_bytes), 0))
+    return SSD_ERR_INVALID_ARG;
+  const bool in_place = grad_hidden == hidden && (rows_per_batch == 1 || row_stride == D) &&
+                        (n_batch == 1 || batch_stride == static_cast<int64_t>(rows_per_batch) * D);
+  const long long extent = 2 * ((n_batch - 1) * batch_stride + (rows_per_batch - 1) * row_stride + D);
+  const bool within = !in_place && overlaps(grad_hidden, gh_bytes, hidden, 1, extent, 0);
+  for (int b = 0; within && b < (batch_stride > 0 ? n_batch : 1); ++b)
+    if (overlaps(grad_hidden, gh_bytes, static_cast<const char*>(hidden) + 2 * b * batch_stride, rows_per_batch, 2ll * D,
+                 2 * row_stride))
+      return SSD_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   PrepArgs a;
   prep_args(&a, p, ws, RowsIn{hidden, batch_stride, row_stride, rows_per_batch}, targets, N, V, D);

@@ -192,6 +192,55 @@ def test_distill_scales_that_are_not_finite(dtype):
 
 
 # ---------------------------------------------------------------------------
+# Outputs over inputs.
+# ---------------------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [6, 200])
+def test_linear_gradients_over_inputs(N):
+    """Over the weight, one another, or parts of the hidden states: refused.  In
+    the gaps of strided inputs, and over a dense hidden itself: allowed."""
+    D, V = 64, 300
+    hidden, weight, targets = linear_case((N,), D, V, 86, keep=0.6)
+    targets[0] = 3
+    r = ssd.ssd_linear_ce(hidden, weight, targets)
+    want = ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse)
+    big = torch.zeros(2 * (N + V), D, device="cuda", dtype=BF16)
+
+    def refused(h, w, **out):
+        with pytest.raises(ssd.SsdError, match="invalid argument"):
+            ssd.ssd_linear_ce_grad(h, w, targets, r.lse, **out)
+
+    refused(hidden, weight, grad_weight=weight)
+    w = big[:V]
+    w.copy_(weight)
+    refused(hidden, w, grad_weight=big[V - 1:2 * V - 1])
+    refused(hidden, w, grad_hidden=big[V - 1:V - 1 + N])
+    refused(hidden, weight, grad_weight=big[:V], grad_hidden=big[V - 1:V - 1 + N])
+    h = big[V:V + N]
+    h.copy_(hidden)
+    refused(h, weight, grad_hidden=big[V + 1:V + 1 + N])
+    refused(h, weight, grad_hidden=big[V - N + 1:V + 1])
+    pair = torch.zeros(V, 2, D, device="cuda", dtype=BF16)      # weight rows with a gap of one row between
+    pair[:, 1] = weight
+    refused(hidden, pair[:, 1], grad_weight=pair.view(2 * V, D)[:V])
+    assert torch.equal(pair[:, 1], weight) and (pair[:, 0] == 0).all()
+    # beside one another
+    g = ssd.ssd_linear_ce_grad(h, w, targets, r.lse, grad_hidden=big[V + N:V + 2 * N],
+                               grad_weight=big[V + 2 * N:2 * V + 2 * N])
+    assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+    # a gap of the hidden batches' stride holds the gradient
+    gap = torch.zeros(4, N, D, device="cuda", dtype=BF16)
+    gap[0], gap[3] = hidden, hidden
+    both, two = gap[::3], torch.stack([targets, targets])
+    lse = torch.stack([r.lse, r.lse])
+    g = ssd.ssd_linear_ce_grad(both, weight, two, lse, grad_hidden=gap[1:3])
+    assert torch.equal(g[0][0], want[0]) and torch.equal(g[0][1], want[0])
+    # in place
+    g = ssd.ssd_linear_ce_grad(h, weight, targets, r.lse, grad_hidden=h)
+    assert torch.equal(h, want[0]) and torch.equal(g[1], want[1])
+
+
+# ---------------------------------------------------------------------------
 # Waits that give up: a build whose product kernel waits 200 ns past its first
 # polls (of up to 100 us each) instead of 2 s.  The first tile of a head 65536
 # wide takes longer than that, so its epilogue gives up; the copies and products
