@@ -539,6 +539,9 @@ def ssd_cache_lookup(offsets: torch.Tensor, tokens: torch.Tensor, k: torch.Tenso
 # ---------------------------------------------------------------------------
 # Draft training.
 # ---------------------------------------------------------------------------
+_INT_MAX = 2 ** 31 - 1      # sizes cross the C entries as int; ctypes would wrap a larger one
+
+
 def _rows_of(t: torch.Tensor, name: str):
     """(n_batch, rows_per_batch, V, batch_stride, row_stride) of a [V], [R, V]
     or [B, R, V] view whose last dimension is dense."""
@@ -550,6 +553,8 @@ def _rows_of(t: torch.Tensor, name: str):
     n = len(shape)
     if n not in (1, 2, 3):
         raise ValueError(f"{name} must have one to three dimensions, got {n}")
+    if max(shape) > _INT_MAX:
+        raise ValueError(f"{name} has a dimension above 2^31 - 1: {tuple(shape)}")
     if shape[-1] > 1 and stride[-1] != 1:
         raise ValueError(f"{name} must be dense in its last dimension")
     if n == 3:
@@ -613,7 +618,7 @@ def ssd_teacher_top(logits: torch.Tensor, M: int, T: float = 1.0, workspace: Opt
     ssd_teacher_top in ssd.h); arrays of shape logits.shape[:-1] (+ (M,))."""
     nb, rpb, V, bs, rs = _rows_of(logits, "logits")
     dt, dev, lead = _logit_dtype(logits), logits.device, tuple(logits.shape[:-1])
-    M = int(M)
+    M = min(int(M), MAX_TOP + 1)      # refused below, whatever the size
     wide = lead + (max(M, 0),)
 
     def call(st):
@@ -672,7 +677,7 @@ def ssd_distill(logits: torch.Tensor, tokens: torch.Tensor, values: torch.Tensor
         loss = torch.empty_like(known) if known is not None else \
             torch.empty(tuple(lead), dtype=torch.float32, device=dev)
         r = DistillResult(loss=loss, status=torch.empty_like(loss, dtype=torch.int32), grad=g)
-        _check(load().ssd_distill(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, M, tokens.data_ptr(),
+        _check(load().ssd_distill(logits.data_ptr(), dt, nb, rpb, V, bs, rs, T, min(M, MAX_TOP + 1), tokens.data_ptr(),
                                   values.data_ptr(), _ptr(tail), _ptr(row_scale), r.loss.data_ptr(),
                                   r.status.data_ptr(), _ptr(g), gbs, grs, st), "ssd_distill")
         return r
@@ -692,7 +697,7 @@ def _linear_args(hidden, weight, targets):
         raise ValueError("hidden and weight must be torch.bfloat16")
     if weight.get_device() != dev.index:
         raise ValueError(f"weight must be on {dev}, got {weight.device}")
-    if weight.dim() != 2 or weight.shape[1] != D or weight.stride(1) != 1:
+    if weight.dim() != 2 or weight.shape[1] != D or weight.stride(1) != 1 or weight.shape[0] > _INT_MAX:
         raise ValueError(f"weight must be [V, {D}] and dense in its last dimension")
     lead = hidden.shape[:-1]
     _want(targets, "targets", torch.int32, lead, dev.index)

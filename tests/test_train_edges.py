@@ -191,6 +191,25 @@ def test_distill_scales_that_are_not_finite(dtype):
     assert torch.equal(r.grad[[0, 3]], e.grad[[0, 3]])
 
 
+@pytest.mark.gpu
+def test_sizes_that_no_int_holds():
+    """Refused, not taken modulo 2^32 (views of a few bytes: nothing of such a size is allocated)."""
+    z = logits_like((1,), 8, BF16, 87)
+    n = 2 ** 32 + 1
+    for big in (z.expand(n, 8), z[None].expand(n, 1, 8), z[None].expand(1, n, 8)):
+        with pytest.raises(ValueError, match="dimension above"):
+            ssd.ssd_teacher_top(big, 1)
+        with pytest.raises(ValueError, match="dimension above"):
+            ssd.ssd_distill(big, z, z)
+        with pytest.raises(ValueError, match="dimension above"):
+            ssd.ssd_linear_ce(big, z, z)
+    for M in (2 ** 32 + 1, 257, 2 ** 31):
+        with pytest.raises(ssd.SsdError, match="invalid argument"):
+            ssd.ssd_teacher_top(z, M)
+    with pytest.raises(ValueError, match="weight must be"):
+        ssd.ssd_linear_ce(z, z.expand(n, 8), torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
 # ---------------------------------------------------------------------------
 # Outputs over inputs.
 # ---------------------------------------------------------------------------
