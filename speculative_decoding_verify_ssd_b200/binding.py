@@ -583,6 +583,8 @@ def _launch(index: int, stream, call):
     given, as the stream that the call's own allocations belong to."""
     if stream is None and torch.cuda.current_device() == index:
         return call(_raw_stream(index))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream must be on cuda:{index}, got {stream.device}")
     with torch.cuda.device(index), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
         return call(_raw_stream(index))
 

@@ -210,6 +210,18 @@ def test_sizes_that_no_int_holds():
         ssd.ssd_linear_ce(z, z.expand(n, 8), torch.zeros(1, dtype=torch.int32, device="cuda"))
 
 
+def test_stream_of_another_device():
+    """Its launch would go to that device's default stream with this one's pointers."""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    def never(raw):
+        raise AssertionError("launched")
+
+    with pytest.raises(ValueError, match="stream must be on cuda:0"):
+        ssd._launch(0, Stream(), never)
+
+
 # ---------------------------------------------------------------------------
 # Outputs over inputs.
 # ---------------------------------------------------------------------------
