@@ -222,6 +222,49 @@ def test_stream_of_another_device():
         ssd._launch(0, Stream(), never)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [3001, 140001])
+def test_distill_rows_with_all_mass_on_one_side(dtype, V):
+    """The whole gradient of rows whose atoms, or whose tail, have no student mass."""
+    T = 1.0
+    tokens, values, tail = teacher((4,), V, 6, T, 88, True)
+    for use_tail in (tail, None):
+        none = logits_like((4,), V, dtype, 89).scatter_(1, tokens.long(), -math.inf)
+        r = check_distill(none, tokens, values, use_tail, T)
+        assert (r.loss == math.inf).all() and (r.status == ssd.ROW_ZERO_Q).all()
+        only = torch.full_like(none, -math.inf).scatter_(1, tokens.long(), 0.25)
+        r = check_distill(only, tokens, values, use_tail, T)
+        rest = torch.ones_like(only, dtype=torch.bool).scatter_(1, tokens.long(), False)
+        assert (r.grad[rest] == 0).all()
+        if use_tail is not None:
+            assert (r.loss == math.inf).all() and (r.status == ssd.ROW_ZERO_Q).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V,dtype", [(262143, BF16), (131075, FP32)])
+def test_distill_more_clusters_than_the_gpu_holds(V, dtype):
+    """Rows of eight blocks each, several times what runs at once; loss and gradient, in place too."""
+    z = logits_like((300,), V, dtype, 90)
+    tokens, values, tail = teacher((300,), V, 33, 1.0, 91, True)
+    r = check_distill(z, tokens, values, tail, 1.0)
+    again = ssd.ssd_distill(z, tokens, values, tail, grad=z)
+    assert torch.equal(again.loss, r.loss) and torch.equal(again.grad, r.grad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,D,V", [(64, 1024, 32000), (700, 1024, 32003), (5000, 64, 60001)])
+def test_linear_repeats_its_bits(N, D, V):
+    hidden, weight, targets = linear_case((N,), D, V, 92, keep=0.8)
+    first = None
+    for _ in range(5):
+        r = ssd.ssd_linear_ce(hidden, weight, targets)
+        g = ssd.ssd_linear_ce_grad(hidden, weight, targets, r.lse)
+        out = (r.loss, r.lse, g[0], g[1])
+        first = first or out
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
 # ---------------------------------------------------------------------------
 # Outputs over inputs.
 # ---------------------------------------------------------------------------
