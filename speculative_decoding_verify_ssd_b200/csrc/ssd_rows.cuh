@@ -349,6 +349,10 @@ struct __align__(16) DistillPart {
   int flags;
 };
 
+// Log-weights, relative to the largest, at and below which e^x is 0 in 64 bits:
+// such a teacher's token has no weight.
+constexpr double kNoWeight = -745.0;
+
 // The teacher's weights: p_m = exp((t_m - top) / T) / total, p_tail likewise.
 struct DistillTeacher {
   double top, total;  // top in units of logits / T
@@ -537,7 +541,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
       if (!is_number(am)) am = 0.f;
       as = warp_sum(ex2((z_atom - am) * c));
       weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
-      num = warp_sum_d(mine && p > 0.f ? static_cast<double>(p) * (t_rel - static_cast<double>(z_atom) * invT) : 0.0);
+      // (at q = 0 any weight makes the loss infinite, one below fp32's range too)
+      const float counts = p > 0.f || z_atom > -INFINITY || !(t_rel > kNoWeight) ? p : 1.f;
+      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - static_cast<double>(z_atom) * invT) : 0.0);
     }
     flags = __reduce_or_sync(0xFFFFFFFFu, flags) | teacher.flags;
     if (flags) sum = __int_as_float(0x7FC00000);
@@ -661,7 +667,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     if (lane == 0) {
       const double p_tail = static_cast<double>(teacher.p_tail);
       double loss = num + weight * (lse - norm);
-      if (p_tail > 0.0) loss += p_tail * (static_cast<double>(tail_in) - teacher.top - norm - lse_tail + lse);
+      const bool any = lse_tail > -INFINITY ? p_tail > 0.0 : static_cast<double>(tail_in) - teacher.top > kNoWeight;
+      if (any && !(p_tail > 0.0))
+        loss = INFINITY;  // as above
+      else if (any)
+        loss += p_tail * (static_cast<double>(tail_in) - teacher.top - norm - lse_tail + lse);
       if (!(total_d > 0.0)) fl |= SSD_ROW_NONFINITE;
       if (!bad && !(loss < INFINITY)) fl |= SSD_ROW_ZERO_Q;
       a.loss[row] = bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);

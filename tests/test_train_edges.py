@@ -13,7 +13,7 @@ from speculative_decoding_verify_ssd_b200 import binding as ssd
 
 from test_train_linear import check as check_linear
 from test_train_rows import check_distill, check_top, teacher
-from train_testlib import linear_case, linear_ref, logits_like, top_ref
+from train_testlib import HALF_STEP, U32, distill_ref, linear_case, linear_ref, logits_like, sum_error, top_ref
 
 BF16, FP32 = torch.bfloat16, torch.float32
 TRAIN_CU = os.path.join(_build.CSRC, "ssd_train.cu")
@@ -239,6 +239,31 @@ def test_distill_rows_with_all_mass_on_one_side(dtype, V):
         assert (r.grad[rest] == 0).all()
         if use_tail is not None:
             assert (r.loss == math.inf).all() and (r.status == ssd.ROW_ZERO_Q).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_distill_weights_below_fp32(dtype):
+    """Atoms and a tail of a weight that only 64 bits hold, where the student has
+    none: infinite; without any weight (masked by the type's lowest value): not."""
+    V = 40
+    tokens = torch.arange(4, dtype=torch.int32, device="cuda").repeat(6, 1)
+    values = torch.zeros(6, 4, device="cuda")
+    tail = torch.zeros(6, device="cuda")
+    z = logits_like((6,), V, dtype, 93)
+    z[:3, 2] = -math.inf
+    z[3:, 4:] = -math.inf
+    for r, at in enumerate((-150.0, -2000.0, torch.finfo(FP32).min)):
+        values[r, 2] = at
+        tail[3 + r] = at
+    r = ssd.ssd_distill(z, tokens, values, tail)
+    f, grad, _ = distill_ref(z, tokens, values, tail, 1.0)
+    assert torch.equal(f == math.inf, torch.tensor([1, 0, 0, 1, 0, 0], device="cuda").bool())
+    assert torch.equal(r.loss == math.inf, f == math.inf)
+    assert torch.equal(r.status, torch.where(f == math.inf, ssd.ROW_ZERO_Q, 0).int())
+    fin = f.isfinite()
+    assert ((r.loss.double() - f).abs()[fin] <= 2 * sum_error(V, dtype) + f[fin] * U32).all()
+    assert ((r.grad.double() - grad).abs() <= 2 * sum_error(V, dtype) + grad.abs() * HALF_STEP[dtype]).all()
 
 
 @pytest.mark.gpu
