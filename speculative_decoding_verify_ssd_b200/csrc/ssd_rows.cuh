@@ -340,7 +340,9 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& v, const GradScale& g)
 
 // What one warp, and then one CTA, of a distillation row found: sums of
 // exponentials of its tail logits and atoms around their maxima (tail_sum NaN:
-// the row is void), and for the loss sum_m p_m ((t_m - top) - z_m) / T and sum_m p_m.
+// the row is void), and for the loss sum_m p_m ((t_m - top) - (z_m - atom_max)) / T
+// and sum_m p_m.  (Around a logit of the row: where all are the type's lowest
+// value, their differences are all that is left of them.)
 // (The loss takes the sum of the p_m as they were rounded: their errors then
 // enter with the size of log p - log q, not of log q.)
 struct __align__(16) DistillPart {
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
       weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
       // (at q = 0 any weight makes the loss infinite, one below fp32's range too)
       const float counts = p > 0.f || z_atom > -INFINITY || !(t_rel > kNoWeight) ? p : 1.f;
-      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - static_cast<double>(z_atom) * invT) : 0.0);
+      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - (static_cast<double>(z_atom) - static_cast<double>(am)) * invT) : 0.0);
     }
     flags = __reduce_or_sync(0xFFFFFFFFu, flags) | teacher.flags;
     if (flags) sum = __int_as_float(0x7FC00000);
@@ -564,7 +566,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const int fl = __reduce_or_sync(0xFFFFFFFFu, q.flags);
     const float ts = warp_sum8(q.tail_sum > 0.f ? q.tail_sum * ex2((q.tail_max - tm) * c) : 0.f);
     const float as = warp_sum8(q.atom_sum > 0.f ? q.atom_sum * ex2((q.atom_max - am) * c) : 0.f);
-    const double num = warp_sum8(q.numer), weight = warp_sum8(q.weight);
+    const double around = am > -INFINITY ? static_cast<double>(am) : 0.0;
+    const double num = warp_sum8(
+        q.weight > 0.0 ? q.numer - q.weight * ((static_cast<double>(q.atom_max) - around) * invT) : q.numer);
+    const double weight = warp_sum8(q.weight);
     const DistillPart out = {tm, fl ? __int_as_float(0x7FC00000) : ts, am, as, num, weight, fl};
     if (lane < C && (lane == 0 || dst)) {
       const uint32_t to = cluster_addr(&parts[rank], lane), on = cluster_addr(&parts_bar, lane);
@@ -652,7 +657,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
         warp_sum8(on && q.y > 0.f ? static_cast<double>(q.y) * static_cast<double>(ex2((q.x - tail_max) * c)) : 0.0);
     const double atom_d =
         warp_sum8(on && q.w > 0.f ? static_cast<double>(q.w) * static_cast<double>(ex2((q.z - atom_max) * c)) : 0.0);
-    const double num = warp_sum8(on ? own->numer : 0.0), weight = warp_sum8(on ? own->weight : 0.0);
+    const double own_weight = on ? own->weight : 0.0;
+    double num = on ? own->numer : 0.0;
+    if (own_weight > 0.0)
+      num -= own_weight * (((q.z > -INFINITY ? static_cast<double>(q.z) : 0.0) - static_cast<double>(at_top)) * invT);
+    num = warp_sum8(num);
+    const double weight = warp_sum8(own_weight);
     int fl = __reduce_or_sync(0xFFFFFFFFu, on ? own->flags : 0) | late;
     // Both around the larger maximum; the tail's own logarithm is kept where its share underflows.
     const float other = tail_max > atom_max ? atom_max : tail_max;
@@ -660,9 +670,9 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const double total_d = tail_max > atom_max ? tail_d + atom_d * factor : tail_d * factor + atom_d;
     // three logarithms at once
     const double logs = log(lane == 0 ? total_d : (lane == 1 ? tail_d : teacher.total));
-    const double lse = static_cast<double>(at_top) * invT + __shfl_sync(0xFFFFFFFFu, logs, 0);
+    const double lse = __shfl_sync(0xFFFFFFFFu, logs, 0), log_tail = __shfl_sync(0xFFFFFFFFu, logs, 1);  // around at_top, tail_max
     const double lse_tail =
-        tail_d > 0.0 ? static_cast<double>(tail_max) * invT + __shfl_sync(0xFFFFFFFFu, logs, 1) : -INFINITY;
+        tail_d > 0.0 ? (static_cast<double>(tail_max) - static_cast<double>(at_top)) * invT + log_tail : -INFINITY;
     const double norm = __shfl_sync(0xFFFFFFFFu, logs, 2);
     if (lane == 0) {
       const double p_tail = static_cast<double>(teacher.p_tail);

@@ -267,6 +267,25 @@ def test_distill_weights_below_fp32(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V,M", [(2, 2), (40, 5), (3001, 70), (140001, 256)])
+@pytest.mark.parametrize("T", [1.0, 0.25])
+def test_distill_rows_of_nothing_but_the_lowest_value(dtype, V, M, T):
+    """A mask of the type's lowest value that leaves nothing: the student is
+    uniform, whatever the size of its logits; and logits of one large value."""
+    tokens, values, tail = teacher((3,), V, M, T, 94, M < V)
+    for at in (torch.finfo(dtype).min, -1e30, 2.0 ** 20):
+        z = torch.full((3, V), at, device="cuda", dtype=dtype)
+        r = ssd.ssd_distill(z, tokens, values, tail, T)
+        f, grad, _ = distill_ref(torch.zeros_like(z), tokens, values, tail, T)
+        e = sum_error(V, dtype)
+        assert (r.status == 0).all()
+        assert ((r.loss.double() - f).abs() <= 2 * e + f.abs() * U32).all()
+        q = 1.0 / V      # an atom's q (2 e of it), then one rounding
+        assert ((r.grad.double() - grad).abs() <= (4 * e * q + 2 * e * grad.abs() * T) / T + grad.abs() * HALF_STEP[dtype]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("V,dtype", [(262143, BF16), (131075, FP32)])
 def test_distill_more_clusters_than_the_gpu_holds(V, dtype):
     """Rows of eight blocks each, several times what runs at once; loss and gradient, in place too."""
