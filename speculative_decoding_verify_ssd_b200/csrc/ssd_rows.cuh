@@ -338,11 +338,19 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& v, const GradScale& g)
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// The logit that the loss terms of some atoms are formed around: their largest,
+// or 0 where 64 bits lose nothing by that (2^-29 of log p - log q).  In a row of
+// nothing but the type's lowest value the differences are all that is left;
+// taking the largest always cost 1.5% of the call, this 1.1% (384 rows of 128256
+// bf16 44.7 us without either, 45.4 and 45.2 with them).
+__device__ __forceinline__ float atom_ref(float atom_max, float c) {
+  return atom_max > -INFINITY && fabsf(atom_max) * c > 16777216.f ? atom_max : 0.f;
+}
+
 // What one warp, and then one CTA, of a distillation row found: sums of
 // exponentials of its tail logits and atoms around their maxima (tail_sum NaN:
-// the row is void), and for the loss sum_m p_m ((t_m - top) - (z_m - atom_max)) / T
-// and sum_m p_m.  (Around a logit of the row: where all are the type's lowest
-// value, their differences are all that is left of them.)
+// the row is void), and for the loss sum_m p_m ((t_m - top) - (z_m - r)) / T and
+// sum_m p_m, with r = atom_ref(atom_max).
 // (The loss takes the sum of the p_m as they were rounded: their errors then
 // enter with the size of log p - log q, not of log q.)
 struct __align__(16) DistillPart {
@@ -545,7 +553,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
       weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
       // (at q = 0 any weight makes the loss infinite, one below fp32's range too)
       const float counts = p > 0.f || z_atom > -INFINITY || !(t_rel > kNoWeight) ? p : 1.f;
-      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - (static_cast<double>(z_atom) - static_cast<double>(am)) * invT) : 0.0);
+      const float around = atom_ref(am, c);
+      double z = static_cast<double>(z_atom);
+      if (__any_sync(0xFFFFFFFFu, around != 0.f)) z -= static_cast<double>(around);  // a branch, rarely taken
+      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - z * invT) : 0.0);
     }
     flags = __reduce_or_sync(0xFFFFFFFFu, flags) | teacher.flags;
     if (flags) sum = __int_as_float(0x7FC00000);
@@ -566,10 +577,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const int fl = __reduce_or_sync(0xFFFFFFFFu, q.flags);
     const float ts = warp_sum8(q.tail_sum > 0.f ? q.tail_sum * ex2((q.tail_max - tm) * c) : 0.f);
     const float as = warp_sum8(q.atom_sum > 0.f ? q.atom_sum * ex2((q.atom_max - am) * c) : 0.f);
-    const double around = am > -INFINITY ? static_cast<double>(am) : 0.0;
-    const double num = warp_sum8(
-        q.weight > 0.0 ? q.numer - q.weight * ((static_cast<double>(q.atom_max) - around) * invT) : q.numer);
-    const double weight = warp_sum8(q.weight);
+    const float around = atom_ref(am, c), own = atom_ref(q.atom_max, c);
+    if (__any_sync(0xFFFFFFFFu, own != around))
+      q.numer -= q.weight * ((static_cast<double>(own) - static_cast<double>(around)) * invT);
+    const double num = warp_sum8(q.numer), weight = warp_sum8(q.weight);
     const DistillPart out = {tm, fl ? __int_as_float(0x7FC00000) : ts, am, as, num, weight, fl};
     if (lane < C && (lane == 0 || dst)) {
       const uint32_t to = cluster_addr(&parts[rank], lane), on = cluster_addr(&parts_bar, lane);
@@ -658,11 +669,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const double atom_d =
         warp_sum8(on && q.w > 0.f ? static_cast<double>(q.w) * static_cast<double>(ex2((q.z - atom_max) * c)) : 0.0);
     const double own_weight = on ? own->weight : 0.0;
-    double num = on ? own->numer : 0.0;
-    if (own_weight > 0.0)
-      num -= own_weight * (((q.z > -INFINITY ? static_cast<double>(q.z) : 0.0) - static_cast<double>(at_top)) * invT);
-    num = warp_sum8(num);
-    const double weight = warp_sum8(own_weight);
+    double numer = on ? own->numer : 0.0, top = static_cast<double>(at_top) * invT;  // top: what the terms leave to it
+    if (__any_sync(0xFFFFFFFFu, atom_ref(q.z, c) != 0.f)) {
+      if (on) numer -= own_weight * ((static_cast<double>(atom_ref(q.z, c)) - static_cast<double>(at_top)) * invT);
+      top = 0.0;
+    }
+    const double num = warp_sum8(numer), weight = warp_sum8(own_weight);
     int fl = __reduce_or_sync(0xFFFFFFFFu, on ? own->flags : 0) | late;
     // Both around the larger maximum; the tail's own logarithm is kept where its share underflows.
     const float other = tail_max > atom_max ? atom_max : tail_max;
@@ -676,7 +688,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
     const double norm = __shfl_sync(0xFFFFFFFFu, logs, 2);
     if (lane == 0) {
       const double p_tail = static_cast<double>(teacher.p_tail);
-      double loss = num + weight * (lse - norm);
+      double loss = num + weight * (lse + top - norm);
       const bool any = lse_tail > -INFINITY ? p_tail > 0.0 : static_cast<double>(tail_in) - teacher.top > kNoWeight;
       if (any && !(p_tail > 0.0))
         loss = INFINITY;  // as above
