@@ -370,7 +370,8 @@ ssd_status ssd_cache_lookup(const int32_t* offsets, const int32_t* tokens, int B
  *   sum_v exp(l(v)/T); tail [rows] out: the same sum over the tokens that are
  *   not among the M (-inf when there are none), formed without subtraction.
  *   1 <= M <= min(V, SSD_MAX_TOP).  status [rows] out: SSD_ROW_NONFINITE for a
- *   row with a NaN or +inf logit or all of -inf (tokens -1, the rest NaN).
+ *   row with a NaN or +inf logit or all of -inf, SSD_ROW_DEVICE_TIMEOUT (an
+ *   error of the GPU: a wait gave up): tokens -1, the rest NaN.
  *   workspace: ssd_teacher_top_workspace_bytes() bytes, 256-byte aligned; it
  *   needs no initial contents, and calls that overlap on the GPU must not
  *   share one.

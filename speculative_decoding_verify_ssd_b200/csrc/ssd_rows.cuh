@@ -93,9 +93,6 @@ struct Elem<float> {
     f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
     f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
   static __device__ __forceinline__ float vec_max(const uint4& v) {
     return fmax_nan(fmax_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
                     fmax_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
@@ -407,9 +404,9 @@ struct DistillArgs {
 // Each of a slice's phases (load, maximum, exponentials, exchange, exponentials
 // again, store) is bound by something else, and they follow one another in a
 // CTA: four CTAs of 52 KB slices per SM overlap part of them.  384 rows of
-// 128256 bf16 with gradient take 45.3 us (4.4 TB/s of logits and gradient, 67%
-// of the copy rate; issue 50%, exp2 pipe 49%), 2048 rows of 151936 256 us
-// (4.9 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
+// 128256 bf16 with gradient take 45.2 us (4.4 TB/s of logits and gradient, 67%
+// of the copy rate; issue 53%, exp2 pipe 53%), 2048 rows of 151936 249-259 us
+// (4.8-5.0 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
 // the next row, and a gradient stored in bulk all measured slower.
 // ---------------------------------------------------------------------------
 template <typename TIn>

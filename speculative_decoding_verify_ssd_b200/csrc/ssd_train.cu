@@ -61,7 +61,10 @@ static ssd_status launch_dependent(void (*fn)(P...), dim3 grid, int threads, int
 // ---------------------------------------------------------------------------
 // Rows in cluster shared memory.
 // ---------------------------------------------------------------------------
-constexpr long long kSliceTarget = 52 * 1024;  // bytes of a row that one CTA stages: four CTAs fit an SM
+// Bytes of a row that one CTA stages.  Four such CTAs of the distillation fit an
+// SM; of the top kernel, whose own shared memory is larger, four up to slices of
+// 51,456 bytes (128256 bf16 gives 51,312) and three above.
+constexpr long long kSliceTarget = 52 * 1024;
 constexpr long long kSliceMin = 8 * 1024;      // do not split a row finer than this for the sake of few rows
 constexpr long long kSliceMax = 200 * 1024;
 constexpr int kSmCount = 148;
@@ -106,9 +109,11 @@ static bool top_plan(long long rows, int V, int esize, TopPlan* p) {
   const long long fill = (kRowFill + rows - 1) / rows, by_len = bytes / kSliceMin;
   const long long extra = fill < by_len ? fill : by_len;
   if (n < extra) n = extra;
-  // One slice, and no join, where that costs less: 80 rows of 125 KB 13.7 us
-  // against 18.5, 384 of 62 KB 16.5 against 23.9; but 384 of 195 KB 43 against
-  // 33 (and 97 KB the same).
+  // One slice, and no join, where that costs less: 384 rows of 62 KB 16.5 us
+  // against 23.9; but 384 of 195 KB 43 against 33 (and 97 KB the same).  Few rows
+  // in one slice against several, 64 logits kept: 1, 32 and 148 of 125 KB 13.9,
+  // 15.0 and 17.0 us against 15.0, 19.4 and 18.8; of 199 KB bf16 16.0, 18.2 and
+  // 21.5 against 14.7, 20.7 and 22.3 (fp32, and 200 kept: less in one).
   if (bytes <= kRowOne || (rows <= kSmCount && bytes <= kSliceMax)) n = 1;
   if (n > kTopSlices) n = kTopSlices;
   const long long need = (bytes + kSliceMax - 1) / kSliceMax;
