@@ -410,7 +410,7 @@ size_t ssd_teacher_top_workspace_bytes(int rows, int V, int dtype, int M);
  *   tail, all logits -inf, or a teacher without weight), SSD_ROW_BAD_TOKEN (an
  *   id outside [-1, V) or twice in a row): loss NaN, gradient 0.
  *   SSD_ROW_ZERO_Q (informational): q is 0 where p is not; the loss is +inf.
- *   (A p below 2^-126, fp32's range, counts there and nowhere else.)
+ *   (A p below 2^-126, fp32's range, counts at logits below -1e30 only.)
  *   SSD_ROW_DEVICE_TIMEOUT (an error of the GPU: a wait gave up after 1 s and
  *   more): loss NaN, gradient 0, or NaN in the places of a thread block that
  *   gave up by itself, whether or not the status tells.

@@ -339,7 +339,8 @@ __device__ __forceinline__ uint4 gradient_of(const uint4& v, const GradScale& g)
 // or 0 where 64 bits lose nothing by that (2^-29 of log p - log q).  In a row of
 // nothing but the type's lowest value the differences are all that is left;
 // taking the largest always cost 1.5% of the call, this 1.1% (384 rows of 128256
-// bf16 44.7 us without either, 45.4 and 45.2 with them).
+// bf16 44.7 us without either, 45.4 and 45.2 with them; small_weight below costs
+// up to 0.6% more).
 __device__ __forceinline__ float atom_ref(float atom_max, float c) {
   return atom_max > -INFINITY && fabsf(atom_max) * c > 16777216.f ? atom_max : 0.f;
 }
@@ -359,6 +360,15 @@ struct __align__(16) DistillPart {
 // Log-weights, relative to the largest, at and below which e^x is 0 in 64 bits:
 // such a teacher's token has no weight.
 constexpr double kNoWeight = -745.0;
+
+// A weight below fp32's range, e^log_weight * inv_total.  It counts at logits this
+// low: where q is 0 the loss is infinite, and the type's lowest value is large
+// enough to be seen.
+constexpr float kMasked = -1e30f;
+__device__ __forceinline__ double small_weight(double log_weight, float inv_total) {
+  const float e = ex2(fmaxf(static_cast<float>(log_weight * 1.4426950408889634) + 126.f, -126.f)) * inv_total;
+  return static_cast<double>(e) * 1.1754943508222875e-38 + 1e-300;  // 2^-126
+}
 
 // The teacher's weights: p_m = exp((t_m - top) / T) / total, p_tail likewise.
 struct DistillTeacher {
@@ -404,8 +414,8 @@ struct DistillArgs {
 // Each of a slice's phases (load, maximum, exponentials, exchange, exponentials
 // again, store) is bound by something else, and they follow one another in a
 // CTA: four CTAs of 52 KB slices per SM overlap part of them.  384 rows of
-// 128256 bf16 with gradient take 45.2 us (4.4 TB/s of logits and gradient, 67%
-// of the copy rate; issue 53%, exp2 pipe 53%), 2048 rows of 151936 249-259 us
+// 128256 bf16 with gradient take 45.4 us (4.4 TB/s of logits and gradient, 67%
+// of the copy rate; issue 53%, exp2 pipe 53%), 2048 rows of 151936 252-262 us
 // (4.8-5.0 TB/s).  Smaller slices (five to eight CTAs), clusters that stay and stage
 // the next row, and a gradient stored in bulk all measured slower.
 // ---------------------------------------------------------------------------
@@ -548,12 +558,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
       if (!is_number(am)) am = 0.f;
       as = warp_sum(ex2((z_atom - am) * c));
       weight = warp_sum_d(mine ? static_cast<double>(p) : 0.0);
-      // (at q = 0 any weight makes the loss infinite, one below fp32's range too)
-      const float counts = p > 0.f || z_atom > -INFINITY || !(t_rel > kNoWeight) ? p : 1.f;
       const float around = atom_ref(am, c);
       double z = static_cast<double>(z_atom);
       if (__any_sync(0xFFFFFFFFu, around != 0.f)) z -= static_cast<double>(around);  // a branch, rarely taken
-      num = warp_sum_d(mine && counts > 0.f ? static_cast<double>(counts) * (t_rel - z * invT) : 0.0);
+      double term = mine && p > 0.f ? static_cast<double>(p) * (t_rel - z * invT) : 0.0;
+      const bool small = mine && p == 0.f && z_atom < kMasked && t_rel > kNoWeight;
+      if (__any_sync(0xFFFFFFFFu, small)) term = small ? small_weight(t_rel, teacher.inv_total) * (t_rel - z * invT) : term;
+      num = warp_sum_d(term);
     }
     flags = __reduce_or_sync(0xFFFFFFFFu, flags) | teacher.flags;
     if (flags) sum = __int_as_float(0x7FC00000);
@@ -684,13 +695,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) ssd_distill_kernel(const Disti
         tail_d > 0.0 ? (static_cast<double>(tail_max) - static_cast<double>(at_top)) * invT + log_tail : -INFINITY;
     const double norm = __shfl_sync(0xFFFFFFFFu, logs, 2);
     if (lane == 0) {
-      const double p_tail = static_cast<double>(teacher.p_tail);
+      double p_tail = static_cast<double>(teacher.p_tail);
       double loss = num + weight * (lse + top - norm);
-      const bool any = lse_tail > -INFINITY ? p_tail > 0.0 : static_cast<double>(tail_in) - teacher.top > kNoWeight;
-      if (any && !(p_tail > 0.0))
-        loss = INFINITY;  // as above
-      else if (any)
-        loss += p_tail * (static_cast<double>(tail_in) - teacher.top - norm - lse_tail + lse);
+      const double t_tail = static_cast<double>(tail_in) - teacher.top;
+      if (!(p_tail > 0.0) && lse_tail < kMasked && t_tail > kNoWeight) p_tail = small_weight(t_tail, teacher.inv_total);
+      if (p_tail > 0.0) loss += p_tail * (t_tail - norm - lse_tail + lse);
       if (!(total_d > 0.0)) fl |= SSD_ROW_NONFINITE;
       if (!bad && !(loss < INFINITY)) fl |= SSD_ROW_ZERO_Q;
       a.loss[row] = bad ? __int_as_float(0x7FC00000) : static_cast<float>(loss);

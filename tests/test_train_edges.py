@@ -268,6 +268,28 @@ def test_distill_weights_below_fp32(dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_distill_small_weights_at_the_lowest_value(dtype):
+    """p below 2^-126 times a logit of -3.4e38 is no small number: an atom's, and the tail's."""
+    V, T = 40, 0.25
+    tokens = torch.arange(4, dtype=torch.int32, device="cuda").repeat(4, 1)
+    values = torch.zeros(4, 4, device="cuda")
+    tail = torch.zeros(4, device="cuda")
+    z = logits_like((4,), V, dtype, 95)
+    z[:2, 2] = torch.finfo(dtype).min
+    z[2:, 4:] = torch.finfo(dtype).min
+    for r, log_p in enumerate((-88.0, -90.0)):
+        values[r, 2] = log_p * T
+        tail[2 + r] = log_p
+    r = ssd.ssd_distill(z, tokens, values, tail, T)
+    f, grad, _ = distill_ref(z, tokens, values, tail, T)
+    assert (r.status == 0).all() and (f > 1.0).all()
+    # the small weight's exponent, up to 2^8 in size, is rounded to 32 bits (2^-16), e^x adds 2^-22
+    assert ((r.loss.double() - f).abs() <= 2 * sum_error(V, dtype) + f * (2.0 ** -16 + 2.0 ** -21)).all()
+    assert ((r.grad.double() - grad).abs() <= 4 * sum_error(V, dtype) / T + grad.abs() * HALF_STEP[dtype]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("V,M", [(2, 2), (40, 5), (3001, 70), (140001, 256)])
 @pytest.mark.parametrize("T", [1.0, 0.25])
 def test_distill_rows_of_nothing_but_the_lowest_value(dtype, V, M, T):
